@@ -68,7 +68,12 @@ extern "C" {
 #define CT_ERR_TUNE_FAILED (-6)  /* no candidate of the search ran correctly  */
 
 /* ---- enums ------------------------------------------------------------ */
-enum ct_dtype { CT_F32 = 0, CT_F16 = 1, CT_BF16 = 2 };
+enum ct_dtype {
+    CT_F32 = 0,
+    CT_F16 = 1,
+    CT_BF16 = 2,
+    CT_E4M3 = 3  /* OCP 8-bit float; transformer-block rows only (below)      */
+};
 enum ct_epilogue { CT_EPI_NONE = 0, CT_EPI_BIAS = 1, CT_EPI_EXP_BIAS_RSQRT = 2 };
 enum ct_bcast_op { CT_BC_EXP = 0 };
 enum ct_bcast_mode {
@@ -322,6 +327,108 @@ int ct_conv2d_nchw_depthwise(const void* x, const void* w, float* y,
                              int stride, int pad, int dtype, int epilogue,
                              const float* bias, const float* var, float eps,
                              void* stream);
+
+/* ---- transformer-block rows ------------------------------------------
+ * The dense path of a transformer block when serving: rows are normalised,
+ * brought to 8 bits, and multiplied with weights.
+ *
+ * Rows.  Every matrix here is a run of rows with contiguous elements; ld* is
+ * the distance between rows in elements (>= the row's length, at most 8 MiB
+ * where a product reads more than one row).  Pointers are aligned to their
+ * element; rows that are not multiples of 16 bytes are read at full width all
+ * the same, only the loads that write LDS directly need that alignment.  M =
+ * 0 rows (an empty batch) is a legal call that does nothing.
+ *
+ * 8-bit rows are e4m3 (OCP: largest value 448, NaN, no infinity) with one
+ * fp32 scale a row: the row stands for scale * q.  From a row of values v:
+ *   a = max(max_k |v[k]|, 2^-100),  scale = a / 448,  q[k] = rne_e4m3(v[k] / scale)
+ * A row of zeros has scale 2^-100 / 448 and q = 0; a row with a NaN a NaN
+ * scale; a row with an infinity (and no NaN) an infinite scale and q = 0 at
+ * its finite places, NaN at the others.
+ *
+ * None of these calls allocates, synchronises or needs the device to have
+ * been set up: all may be captured as a stream's first work.  They take no
+ * workspace from the library. */
+
+/* h = x + residual (fp32), y = h * rsqrt(mean_k h^2 + eps) * gain.
+ * x, residual and h are [M][D] of `dtype` (CT_F32, CT_F16 or CT_BF16); gain
+ * is float [D] (NULL: ones).  residual may be NULL; then h is not written and
+ * must be NULL too.  With a residual, h (the new residual stream, rounded to
+ * dtype) may be NULL if it is not wanted; y is made from the unrounded sum.
+ * y [M][D] is of out_dtype: CT_F32, CT_F16 or CT_BF16 (scale is NULL), or
+ * CT_E4M3 with scale float [M].  Sums are fp32.  h and y may each be exactly x
+ * or residual (same pointer, stride and type); no other overlap.
+ * Errors: CT_ERR_INVALID_ARG for M < 0, D < 1, a NULL or misaligned pointer,
+ * a stride below D, an unknown dtype, h without residual, scale missing (or
+ * given without CT_E4M3), or eps negative or not finite; CT_ERR_HIP on a
+ * launch failure.  Asynchronous on `stream`. */
+int ct_rmsnorm_fwd(const void* x, long long ldx, const void* residual, long long ldr,
+                   const float* gain, void* h, long long ldh, void* y, long long ldy,
+                   float* scale, int M, int D, int dtype, int out_dtype, float eps,
+                   void* stream);
+
+/* Rows x [M][D] (CT_F32, CT_F16 or CT_BF16) to e4m3 q [M][D] with scale [M],
+ * as above: a layer's weights once, and activations that no norm produces.
+ * Errors as for ct_rmsnorm_fwd. */
+int ct_quantize_rows(const void* x, long long ldx, void* q, long long ldq, float* scale,
+                     int M, int D, int dtype, void* stream);
+
+enum ct_activation {
+    CT_ACT_NONE = 0,
+    CT_ACT_RELU = 1,
+    CT_ACT_GELU = 2,       /* z (1 + erf(z / sqrt 2)) / 2                     */
+    CT_ACT_GELU_TANH = 3,  /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+    CT_ACT_SILU = 4        /* z / (1 + exp(-z))                               */
+};
+
+/* What a product does with its sums z, in this order:
+ *   y = act(z + bias[n]) * gate[m][n] + residual[m][n]
+ * gate and residual are [M][N] of y's type; NULL members are left out.  y may
+ * be exactly gate or residual (same pointer and stride); no other overlap.
+ * All of it is fp32, with one rounding, to y's type. */
+typedef struct ct_linear_epilogue {
+    int act;              /* ct_activation */
+    const float* bias;    /* [N] */
+    const void* gate;
+    long long ldg;
+    const void* residual;
+    long long ldr;
+} ct_linear_epilogue;
+
+/* Linear layer y = epilogue(x w^T):
+ *   z[m][n] = sum_{k<K} x[m][k] * w[n][k]
+ * x [M][K] and w [N][K] of `dtype` (CT_F32, CT_F16 or CT_BF16), y [M][N] of
+ * out_dtype (the same three), sums in fp32.  epi may be NULL (y = z).
+ * A product with too few results to fill the device splits its sum over k;
+ * the parts are fp32 and joined in order (the result depends on the sizes
+ * and dtype alone).  They need `workspace`, of at least
+ * ct_linear_workspace_bytes bytes (often 0; then it may be NULL), 16-byte
+ * aligned, written by the call and free again when its work on the stream is
+ * done: calls that may overlap, and graphs that may be replayed at the same
+ * time, need one each.
+ * Errors: CT_ERR_INVALID_ARG for M < 0, N or K < 1, a NULL or misaligned
+ * pointer, a stride below the row's length, an unknown dtype or activation,
+ * or a workspace that is too small; CT_ERR_UNSUPPORTED for M, N or a row's
+ * bytes above 2^30, x or w rows more than 8 MiB apart, or more than 2^31 - 1
+ * tiles; CT_ERR_HIP on a launch failure.  Asynchronous on `stream`. */
+int ct_linear_fwd(const void* x, long long ldx, const void* w, long long ldw,
+                  void* y, long long ldy, int M, int N, int K, int dtype, int out_dtype,
+                  const ct_linear_epilogue* epi, void* workspace, long long workspace_bytes,
+                  void* stream);
+
+/* The same on 8-bit rows: x [M][K] and w [N][K] are CT_E4M3 with row scales
+ * xs [M] and ws [N]:
+ *   z[m][n] = xs[m] * ws[n] * sum_{k<K} x[m][k] * w[n][k] */
+int ct_linear_q8_fwd(const void* x, long long ldx, const float* xs,
+                     const void* w, long long ldw, const float* ws,
+                     void* y, long long ldy, int M, int N, int K, int out_dtype,
+                     const ct_linear_epilogue* epi, void* workspace, long long workspace_bytes,
+                     void* stream);
+
+/* Bytes of workspace a product of these sizes needs (dtype: that of x and w,
+ * CT_E4M3 for ct_linear_q8_fwd); < 0 (a status) for sizes or a dtype the
+ * product refuses.  Host only. */
+long long ct_linear_workspace_bytes(int M, int N, int K, int dtype);
 
 /* ---- tile-config search ----------------------------------------------
  * The space of a shape follows the TVM tutorial's template (Step 1): ordered

@@ -71,15 +71,15 @@ def build(jobs: int | None = None) -> str:
 ASAN_DIR = os.path.join(BUILD, "asan")
 HOST_CHECK = os.path.join(ASAN_DIR, "host_check")
 HOST_CHECK_SRC = os.path.join(ROOT, "tests", "sanitize", "host_check.cpp")
-RUNTIME_SRC = os.path.join(CSRC, "runtime.cpp")
+HOST_SRCS = sorted(glob.glob(os.path.join(CSRC, "*.cpp")))  # the C-ABI runtime
 # sanitizers on the host side only: the device code is built as usual
 SANITIZE = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
             "-Xarch_host", "-fno-sanitize-recover=undefined", "-Xarch_host", "-fno-omit-frame-pointer"]
 
 
 def build_host_check() -> str:
-    """The host-code check binary: the C-ABI runtime (runtime.cpp, all of the
-    library's host logic) built with AddressSanitizer and
+    """The host-code check binary: the C-ABI runtime (runtime.cpp and
+    block_api.cpp, the library's host logic) built with AddressSanitizer and
     UndefinedBehaviorSanitizer on its host side, linked with the kernel
     objects of the regular build and tests/sanitize/host_check.cpp."""
     os.makedirs(ASAN_DIR, exist_ok=True)
@@ -90,15 +90,15 @@ def build_host_check() -> str:
     flags = ["-O1", "-g", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
              "-Wno-unused-command-line-argument", "-I", os.path.join(ROOT, "include"), "-I", CSRC]
-    rt_obj = os.path.join(ASAN_DIR, "runtime.cpp.o")
     main_obj = os.path.join(ASAN_DIR, "host_check.o")
-    for cmd in ([HIPCC] + flags + SANITIZE + ["-x", "hip", "-c", RUNTIME_SRC, "-o", rt_obj],
-                [HIPCC] + flags + SANITIZE + ["-c", HOST_CHECK_SRC, "-o", main_obj]):
+    rt_objs = [os.path.join(ASAN_DIR, os.path.basename(h) + ".o") for h in HOST_SRCS]
+    cmds = [[HIPCC] + flags + SANITIZE + ["-x", "hip", "-c", h, "-o", o] for h, o in zip(HOST_SRCS, rt_objs)]
+    for cmd in cmds + [[HIPCC] + flags + SANITIZE + ["-c", HOST_CHECK_SRC, "-o", main_obj]]:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"sanitized host build failed:\n{r.stderr}")
     tmp = HOST_CHECK + ".tmp"
-    r = subprocess.run([HIPCC, f"--offload-arch={ARCH}"] + SANITIZE + ["-o", tmp, main_obj, rt_obj] + objs,
+    r = subprocess.run([HIPCC, f"--offload-arch={ARCH}"] + SANITIZE + ["-o", tmp, main_obj] + rt_objs + objs,
                        capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"host check link failed:\n{r.stderr}")

@@ -24,10 +24,12 @@ CT_ERR_NO_MEMORY = -4
 CT_ERR_IO = -5
 CT_ERR_TUNE_FAILED = -6
 
-CT_F32, CT_F16, CT_BF16 = 0, 1, 2
+CT_F32, CT_F16, CT_BF16, CT_E4M3 = 0, 1, 2, 3
 # bytes of the no-allocation entry point's fixed scratch (partials and filter copy)
 CT_NOALLOC_SCRATCH_BYTES = 16 << 20
 CT_EPI_NONE, CT_EPI_BIAS, CT_EPI_EXP_BIAS_RSQRT = 0, 1, 2
+CT_ACT_NONE, CT_ACT_RELU, CT_ACT_GELU, CT_ACT_GELU_TANH, CT_ACT_SILU = 0, 1, 2, 3, 4
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 CT_BC_EXP = 0
 CT_BC_AUTO, CT_BC_CHANNEL, CT_BC_FLAT = 0, 1, 2
 CT_CHAIN_MAX_OPS = 8
@@ -52,6 +54,11 @@ class ct_chain_op(ctypes.Structure):
 
 class ct_bcast_program(ctypes.Structure):
     _fields_ = [("n_ops", ctypes.c_int * 3), ("ops", (ct_chain_op * CT_CHAIN_MAX_OPS) * 3)]
+
+
+class ct_linear_epilogue(ctypes.Structure):
+    _fields_ = [("act", ctypes.c_int), ("bias", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("ldg", ctypes.c_longlong), ("residual", ctypes.c_void_p), ("ldr", ctypes.c_longlong)]
 
 
 class ct_tvm_config(ctypes.Structure):
@@ -136,6 +143,11 @@ _SIGS = {
     "ct_gemm_query": (_I, [_I] * 5 + [ctypes.POINTER(ct_tile_config), ctypes.POINTER(_I)]),
     "ct_conv2d_nchw_depthwise": (_I, [_P, _P, _P] + [_I] * 10 + [_P, _P, _F, _P]),
     "ct_broadcast_chain": (_I, [ctypes.POINTER(ct_bcast_program)] + [_P] * 6 + [_I, _LL, _I, _LL, _I, _P]),
+    "ct_rmsnorm_fwd": (_I, [_P, _LL, _P, _LL, _P, _P, _LL, _P, _LL, _P, _I, _I, _I, _I, _F, _P]),
+    "ct_quantize_rows": (_I, [_P, _LL, _P, _LL, _P, _I, _I, _I, _P]),
+    "ct_linear_fwd": (_I, [_P, _LL, _P, _LL, _P, _LL] + [_I] * 5 + [_P, _P, _LL, _P]),
+    "ct_linear_q8_fwd": (_I, [_P, _LL, _P, _P, _LL, _P, _P, _LL] + [_I] * 4 + [_P, _P, _LL, _P]),
+    "ct_linear_workspace_bytes": (_LL, [_I] * 4),
     "ct_variant_count": (_I, []),
     "ct_variant_info": (_I, [_I, ctypes.POINTER(ct_variant_desc)]),
     "ct_split_count": (_LL, [_LL, _I]),
@@ -328,6 +340,39 @@ def ct_broadcast_chain(prog, a0, a1, a2, a3, x, out, out_dtype, outer, P, inner,
                        stream=None) -> int:
     return _load().ct_broadcast_chain(ctypes.byref(prog), _ptr(a0), _ptr(a1), _ptr(a2), _ptr(a3), _ptr(x),
                                       _ptr(out), out_dtype, outer, P, inner, mode, _stream(stream))
+
+
+def _row_ptr(t) -> Optional[int]:
+    """The address of a matrix whose rows may lie apart (or a device pointer)."""
+    return t if t is None or isinstance(t, int) else t.data_ptr()
+
+
+def ct_rmsnorm_fwd(x, ldx, residual, ldr, gain, h, ldh, y, ldy, scale, M, D, dtype, out_dtype, eps=1e-6,
+                   stream=None) -> int:
+    return _load().ct_rmsnorm_fwd(_row_ptr(x), ldx, _row_ptr(residual), ldr, _ptr(gain), _row_ptr(h), ldh,
+                                  _row_ptr(y), ldy, _ptr(scale), M, D, dtype, out_dtype, eps, _stream(stream))
+
+
+def ct_quantize_rows(x, ldx, q, ldq, scale, M, D, dtype, stream=None) -> int:
+    return _load().ct_quantize_rows(_row_ptr(x), ldx, _row_ptr(q), ldq, _ptr(scale), M, D, dtype, _stream(stream))
+
+
+def ct_linear_fwd(x, ldx, w, ldw, y, ldy, M, N, K, dtype, out_dtype, epi: Optional[ct_linear_epilogue] = None,
+                  workspace=None, workspace_bytes=0, stream=None) -> int:
+    return _load().ct_linear_fwd(_row_ptr(x), ldx, _row_ptr(w), ldw, _row_ptr(y), ldy, M, N, K, dtype, out_dtype,
+                                 ctypes.addressof(epi) if epi is not None else None, _ptr(workspace),
+                                 workspace_bytes, _stream(stream))
+
+
+def ct_linear_q8_fwd(x, ldx, xs, w, ldw, ws, y, ldy, M, N, K, out_dtype, epi: Optional[ct_linear_epilogue] = None,
+                     workspace=None, workspace_bytes=0, stream=None) -> int:
+    return _load().ct_linear_q8_fwd(_row_ptr(x), ldx, _ptr(xs), _row_ptr(w), ldw, _ptr(ws), _row_ptr(y), ldy, M, N,
+                                    K, out_dtype, ctypes.addressof(epi) if epi is not None else None,
+                                    _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def ct_linear_workspace_bytes(M, N, K, dtype) -> int:
+    return _load().ct_linear_workspace_bytes(M, N, K, dtype)
 
 
 def ct_conv2d_tune_guided(N, CI, H, W, CO, KH, KW, stride, pad, dtype, epilogue, max_trials=64, batch=8,
@@ -597,6 +642,202 @@ def conv2d_depthwise(x, w, stride: int = 1, pad: int = 0, epilogue: int = CT_EPI
                                   epilogue, bias, var, eps, stream)
     check(st, "conv2d_depthwise")
     return y
+
+
+# ---- transformer-block rows: matrices whose rows may lie apart -------------
+def _matrix(name: str, t, device, dtype=None, shape=None) -> int:
+    """Check a matrix argument; the distance between its rows, in elements."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor on the device of the others")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    rows, cols = t.shape
+    if shape is not None and (rows, cols) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {[rows, cols]}")
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    if rows <= 1:
+        return cols  # a single row has no stride to speak of
+    if ld < cols:
+        raise ValueError(f"{name}: rows must not overlap")
+    return ld
+
+
+def _vector(name: str, t, device, n: int) -> int:
+    """Check an fp32 vector argument; its address."""
+    import torch
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor on the device of the others")
+    if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be {n} contiguous fp32 values")
+    return t.data_ptr()
+
+
+def _place(device, stream):
+    """(context, stream handle): the context makes `device` current and, with
+    an explicit stream, has torch allocate outputs and workspace for that
+    stream; None where nothing has to change."""
+    import torch
+    if stream is None:
+        if device.index == torch.cuda.current_device():
+            return None, torch.cuda.current_stream().cuda_stream
+        return torch.cuda.device(device), torch.cuda.current_stream(device).cuda_stream
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    if stream.device != device:
+        raise ValueError("the stream belongs to another device than the tensors")
+    return torch.cuda.stream(stream), stream.cuda_stream
+
+
+def _placed(device, stream, call, *args):
+    ctx, handle = _place(device, stream)
+    if ctx is None:
+        return call(handle, *args)
+    with ctx:
+        return call(handle, *args)
+
+
+def rmsnorm(x, gain=None, residual=None, eps: float = 1e-6, out_dtype=None, h=True, out=None, scale=None,
+            stream=None):
+    """RMS norm of the rows of x + residual: (y, scale, h).
+
+    y = s * rsqrt(mean(s^2) + eps) * gain, s = x + residual in fp32; y has
+    out_dtype (x's by default), torch.float8_e4m3fn giving 8-bit rows with
+    their scales (None otherwise).  h is s rounded to x's type (the new
+    residual stream; None without a residual or with h=False; h may name the
+    tensor to write, x and residual among them).  x, residual, h and out are
+    [M, D] with contiguous rows; gain is fp32 [D]."""
+    import torch
+    device, dtype = x.device, dtype_code(x.dtype)
+    ldx = _matrix("x", x, device)
+    M, D = x.shape
+    gp = None if gain is None else _vector("gain", gain, device, D)
+    ldr = ldh = 0
+    if residual is not None:
+        ldr = _matrix("residual", residual, device, x.dtype, (M, D))
+    hout = h if isinstance(h, torch.Tensor) else None
+    if hout is not None:
+        if residual is None:
+            raise ValueError("h is the sum with a residual, and there is none")
+        ldh = _matrix("h", hout, device, x.dtype, (M, D))
+    out_dtype = out_dtype or (out.dtype if out is not None else x.dtype)
+    q8 = out_dtype == torch.float8_e4m3fn
+    code = CT_E4M3 if q8 else dtype_code(out_dtype)
+    if out is not None:
+        _matrix("out", out, device, out_dtype, (M, D))
+    if scale is not None:
+        if not q8:
+            raise ValueError("scale belongs to 8-bit output")
+        _vector("scale", scale, device, M)
+
+    def call(handle):
+        y = out if out is not None else torch.empty((M, D), dtype=out_dtype, device=device)
+        sc = scale if scale is not None or not q8 else torch.empty(M, dtype=torch.float32, device=device)
+        ho, ld = hout, ldh
+        if ho is None and residual is not None and h is True:
+            ho, ld = torch.empty((M, D), dtype=x.dtype, device=device), D
+        check(_load().ct_rmsnorm_fwd(
+            x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, gp,
+            None if ho is None else ho.data_ptr(), ld, y.data_ptr(), y.stride(0) if M > 1 else D,
+            None if sc is None else sc.data_ptr(), M, D, dtype, code, eps, handle), "rmsnorm")
+        return y, sc, ho
+
+    return _placed(device, stream, call)
+
+
+def quantize_rows(x, out=None, scale=None, stream=None):
+    """The rows of x [M, D] in 8 bits: (q float8_e4m3fn [M, D], scale fp32 [M]),
+    x ~ scale[:, None] * q."""
+    import torch
+    device, dtype = x.device, dtype_code(x.dtype)
+    ldx = _matrix("x", x, device)
+    M, D = x.shape
+    if out is not None:
+        _matrix("out", out, device, torch.float8_e4m3fn, (M, D))
+    if scale is not None:
+        _vector("scale", scale, device, M)
+
+    def call(handle):
+        q = out if out is not None else torch.empty((M, D), dtype=torch.float8_e4m3fn, device=device)
+        sc = scale if scale is not None else torch.empty(M, dtype=torch.float32, device=device)
+        check(_load().ct_quantize_rows(x.data_ptr(), ldx, q.data_ptr(), q.stride(0) if M > 1 else D, sc.data_ptr(),
+                                       M, D, dtype, handle), "quantize_rows")
+        return q, sc
+
+    return _placed(device, stream, call)
+
+
+def _product(x, xs, w, ws, bias, act, gate, residual, out_dtype, out, stream):
+    import torch
+    device = x.device
+    q8 = xs is not None
+    ldx = _matrix("x", x, device, torch.float8_e4m3fn if q8 else None)
+    ldw = _matrix("w", w, device, x.dtype)
+    M, K = x.shape
+    N, K2 = w.shape
+    if K != K2:
+        raise ValueError(f"x has rows of {K} and w of {K2}")
+    dtype = CT_E4M3 if q8 else dtype_code(x.dtype)
+    if act not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {act!r}: one of {', '.join(ACTIVATIONS)}")
+    if out is not None:
+        _matrix("out", out, device, out_dtype, (M, N))
+        out_dtype = out.dtype
+    elif out_dtype is None:
+        out_dtype = torch.bfloat16 if q8 else x.dtype
+    code = dtype_code(out_dtype)
+    epi = None
+    if act != "none" or bias is not None or gate is not None or residual is not None:
+        epi = ct_linear_epilogue(ACTIVATIONS[act])
+        if bias is not None:
+            epi.bias = _vector("bias", bias, device, N)
+        if gate is not None:
+            epi.ldg = _matrix("gate", gate, device, out_dtype, (M, N))
+            epi.gate = gate.data_ptr()
+        if residual is not None:
+            epi.ldr = _matrix("residual", residual, device, out_dtype, (M, N))
+            epi.residual = residual.data_ptr()
+    if q8:
+        xsp, wsp = _vector("xs", xs, device, M), _vector("ws", ws, device, N)
+
+    def call(handle):
+        lib = _load()
+        y = out if out is not None else torch.empty((M, N), dtype=out_dtype, device=device)
+        ldy = y.stride(0) if M > 1 else N
+        need = lib.ct_linear_workspace_bytes(M, N, K, dtype)
+        space = None if need <= 0 else torch.empty(need, dtype=torch.uint8, device=device)
+        sp, ep = None if space is None else space.data_ptr(), None if epi is None else ctypes.addressof(epi)
+        if q8:
+            st = lib.ct_linear_q8_fwd(x.data_ptr(), ldx, xsp, w.data_ptr(), ldw, wsp, y.data_ptr(), ldy, M, N, K, code,
+                                      ep, sp, max(need, 0), handle)
+        else:
+            st = lib.ct_linear_fwd(x.data_ptr(), ldx, w.data_ptr(), ldw, y.data_ptr(), ldy, M, N, K, dtype, code, ep,
+                                   sp, max(need, 0), handle)
+        check(st, "linear_q8" if q8 else "linear")
+        return y
+
+    return _placed(device, stream, call)
+
+
+def linear(x, w, bias=None, act: str = "none", gate=None, residual=None, out_dtype=None, out=None, stream=None):
+    """y = act(x @ w.T + bias) * gate + residual, rounded once.
+
+    x [M, K] and w [N, K] of one type (fp32, fp16, bf16), rows contiguous; bias
+    fp32 [N]; gate and residual [M, N] of y's type (out_dtype, x's by
+    default); act one of ACTIVATIONS.  out may be gate or residual itself."""
+    return _product(x, None, w, None, bias, act, gate, residual, out_dtype, out, stream)
+
+
+def linear_q8(xq, xs, wq, ws, bias=None, act: str = "none", gate=None, residual=None, out_dtype=None, out=None,
+              stream=None):
+    """linear on 8-bit rows (float8_e4m3fn) with their fp32 scales xs [M] and
+    ws [N]; y has out_dtype (bf16 by default)."""
+    if xs is None or ws is None:
+        raise ValueError("8-bit rows have scales")
+    return _product(xq, xs, wq, ws, bias, act, gate, residual, out_dtype, out, stream)
 
 
 def broadcast(var, N: int, H: int, W: int, out_dtype=None, mode: int = CT_BC_AUTO, out=None,

@@ -1,0 +1,71 @@
+// Host-visible declarations of the transformer-block kernels: the linear
+// layer (linear.hip) and the row operators (rows.hip).  Arguments are checked
+// by the C entry points (block_api.cpp) before they get here.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+namespace ct {
+
+// ---------------------------------------------------------------- linear --
+// y = act(scale * x w^T + bias) * gate + residual (include/convtile.h).
+// Pointers and strides are in bytes: a stage of the reduction is 128 bytes of
+// a row whatever the type.
+struct LinearParams {
+    const char* x;       // [M] rows of K elements, ldx bytes apart
+    const char* w;       // [N] rows of K elements, ldw bytes apart
+    char* y;             // [M] rows of N elements of out_dt
+    const float* bias;   // [N] or null
+    const char* gate;    // [M] rows of N elements of out_dt, or null
+    const char* res;     // the same
+    const float* xs;     // [M], [N] row scales of 8-bit operands, or null
+    const float* ws;
+    float* part;         // [S][M][N] partial sums (S > 1)
+    long long ldx, ldw, ldy, ldg, ldr;  // bytes
+    int M, N;
+    int kbytes;          // bytes of a row of x and w
+    int act, out_dt;
+    int vec;             // y, gate and residual rows are 16-byte aligned
+    int tiles_m, tiles_n;
+    int S, stages_per_split;
+};
+
+// The kernel that runs a product.
+enum LinearForm {
+    LIN_ROW16 = 0,  // at most 16 rows of x: weights straight to registers
+    LIN_ROW32 = 1,  // at most 32
+    LIN_T64 = 2,    // 64 x 64 tiles through LDS
+    LIN_T128 = 3,   // 128 x 128
+    LIN_T256 = 4,   // 256 x 256
+};
+
+struct LinearPlan {
+    int form;
+    int S;  // parts the reduction is split into (tile forms)
+};
+
+// The form and split for a product of these sizes (kbytes: bytes of a row).
+LinearPlan linear_plan(int M, int N, int kbytes, int dtype);
+// p holds everything but the tiling fields, which are filled in here.
+// aligned: rows of x and w are whole numbers of 16 bytes, 16-byte aligned.
+hipError_t launch_linear(const LinearPlan& plan, LinearParams p, int dtype, bool aligned, hipStream_t stream);
+
+// ------------------------------------------------------------------ rows --
+// h = x + residual; y = h * rsqrt(mean h^2 + eps) * gain, or y = h where no
+// norm is asked for; to out_dt, or to e4m3 with a scale a row.
+struct RowsParams {
+    const char* x;
+    const char* res;    // or null
+    const float* gain;  // or null
+    char* h;            // or null
+    char* y;
+    float* scale;       // e4m3 only
+    long long ldx, ldres, ldh, ldy;  // bytes
+    int D;
+    int out_dt;
+    float eps;
+};
+
+hipError_t launch_rows(const RowsParams& p, int M, int dtype, bool norm, hipStream_t stream);
+
+}  // namespace ct

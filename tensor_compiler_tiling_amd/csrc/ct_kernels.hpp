@@ -7,6 +7,10 @@
 
 namespace ct {
 
+// Record a message for ct_last_error() on this thread and return `status`.
+int fail(int status, const char* fmt, ...);
+int hip_fail(hipError_t e, const char* what);
+
 // Division by a runtime constant d (1 <= d < 2^31) with a multiply-high and a
 // shift (Granlund and Montgomery, "Division by invariant integers using
 // multiplication", 1994): q = (umulhi(n, mul) + n) >> shift, exact for every

@@ -1,0 +1,713 @@
+// Linear layer: y = act(scale * x w^T + bias) * gate + residual.
+//
+// x [M][K] and w [N][K] both hold the reduction contiguously, so every type
+// is read the same way, in 16-byte chunks of a row: a chunk is 4 fp32, 8
+// half-precision or 16 e4m3 elements, a stage of the reduction is 128 bytes
+// of every row of a tile, and only the matrix instruction differs.  Which
+// element of the reduction a lane's registers hold does not matter as long as
+// both operands hold the same one, so the chunks go to the instructions as
+// they lie: no operand is rearranged.
+//
+// The weights are the instruction's first operand (its rows) and x the second
+// (its columns): a lane's results then belong to one row of x, and the rows
+// of w are dealt to the instruction's rows so that they are neighbours in it
+// (4, or 16 with 32 x 32 instructions): y, gate and residual are read and
+// written in 16-byte vectors straight from the accumulators' lanes.
+#include "ct_device.hpp"
+#include "block_kernels.hpp"
+
+#include <atomic>
+
+namespace ct {
+
+namespace {
+
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+typedef _Float16 halfx8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef unsigned int uint4v __attribute__((ext_vector_type(4)));
+typedef int int8v __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void lds_void_t;
+
+// 8-bit operands: DT_E4M3 on the 8-bit instruction, which aligns the products
+// of every 8 neighbours of the reduction to the largest of them and cuts what
+// lies 2^-13 below it (a product of 4 beside one of 2^16 is lost whole;
+// measured, with the cut the same on the older 8-bit instructions): sums off by
+// 1.5e-5 of their size in the 2-norm on normally distributed rows, whatever K.
+// That is 1/130 of the rounding of a bf16 result and 1/16 of an fp16 one, for
+// twice the rate.  DT_E4M3_WIDE widens the operands to fp16, exactly, and
+// takes its instruction, whose sums keep fp32: for fp32 results, and for the
+// row forms, which the weights' reading bounds anyway.
+enum { DT_E4M3 = 3, DT_E4M3_WIDE = 4 };
+enum { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SILU = 4 };
+
+constexpr int kBufRaw = 0x00020000;        // raw buffer descriptor
+constexpr unsigned kBufOut = 0x80000000u;  // an offset past every buffer here (all below 2 GiB): reads zeros
+constexpr int kStage = 128;                // bytes of a row a stage
+
+template <int DT> constexpr int elem_size() { return DT == DT_F32 ? 4 : DT >= DT_E4M3 ? 1 : 2; }
+
+__device__ __forceinline__ int8v join(uint4v lo, uint4v hi) {
+    return __builtin_bit_cast(int8v, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// Elements 8 i .. 8 i + 7 of a chunk of 8-bit elements as fp16.
+__device__ __forceinline__ halfx8 widen(uint4v v, int i) {
+    typedef _Float16 halfx2 __attribute__((ext_vector_type(2)));
+    const halfx2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[2 * i], 1.0f, false);
+    const halfx2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[2 * i], 1.0f, true);
+    const halfx2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[2 * i + 1], 1.0f, false);
+    const halfx2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[2 * i + 1], 1.0f, true);
+    return halfx8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// The products of two pairs of chunks, 32 x 32 results: lane l holds chunks of
+// row l % 32 of each operand; lanes l / 32 hold different ones.
+template <int DT>
+__device__ __forceinline__ floatx16 mma32(uint4v a0, uint4v a1, uint4v b0, uint4v b1, floatx16 c) {
+    if constexpr (DT == DT_E4M3) {
+        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join(a0, a1), join(b0, b1), c, 0, 0, 0, 0, 0, 0);
+    } else if constexpr (DT == DT_E4M3_WIDE) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) c = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen(a0, i), widen(b0, i), c, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) c = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen(a1, i), widen(b1, i), c, 0, 0, 0);
+        return c;
+    } else if constexpr (DT == DT_F16) {
+        c = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(halfx8, a0), __builtin_bit_cast(halfx8, b0), c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(halfx8, a1), __builtin_bit_cast(halfx8, b1), c, 0, 0, 0);
+    } else if constexpr (DT == DT_BF16) {
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a0), __builtin_bit_cast(bf16x8, b0), c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a1), __builtin_bit_cast(bf16x8, b1), c, 0, 0, 0);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a0[i]), __uint_as_float(b0[i]), c, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a1[i]), __uint_as_float(b1[i]), c, 0, 0, 0);
+        return c;
+    }
+}
+
+// The same for 16 x 16 results: lane l holds chunks of row l % 16.
+template <int DT>
+__device__ __forceinline__ floatx4 mma16(uint4v a0, uint4v a1, uint4v b0, uint4v b1, floatx4 c) {
+    if constexpr (DT == DT_E4M3_WIDE) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) c = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen(a0, i), widen(b0, i), c, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) c = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen(a1, i), widen(b1, i), c, 0, 0, 0);
+        return c;
+    } else if constexpr (DT == DT_F16) {
+        c = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(halfx8, a0), __builtin_bit_cast(halfx8, b0), c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(halfx8, a1), __builtin_bit_cast(halfx8, b1), c, 0, 0, 0);
+    } else if constexpr (DT == DT_BF16) {
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a0), __builtin_bit_cast(bf16x8, b0), c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a1), __builtin_bit_cast(bf16x8, b1), c, 0, 0, 0);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a0[i]), __uint_as_float(b0[i]), c, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a1[i]), __uint_as_float(b1[i]), c, 0, 0, 0);
+        return c;
+    }
+}
+
+// ---------------------------------------------------------------- epilogue --
+// exp and the reciprocal run on the hardware units, about 1 ulp each.
+__device__ __forceinline__ float sigmoid_times(float z, float u) {
+    return z * __builtin_amdgcn_rcpf(1.0f + dev_exp(-u));
+}
+
+template <int V>
+__device__ __forceinline__ void activate(float (&z)[V], int act) {
+    switch (act) {
+        case ACT_RELU:
+#pragma unroll
+            for (int i = 0; i < V; ++i) z[i] = z[i] < 0.0f ? 0.0f : z[i];  // NaN stays
+            break;
+        case ACT_GELU:
+#pragma unroll
+            for (int i = 0; i < V; ++i) z[i] = 0.5f * z[i] * (1.0f + erff(z[i] * 0.70710678f));
+            break;
+        case ACT_GELU_TANH:
+            // 0.5 (1 + tanh u) = 1 / (1 + exp(-2 u)), u = sqrt(2 / pi) (z + 0.044715 z^3)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                z[i] = sigmoid_times(z[i], 1.5957691f * fmaf(0.044715f * z[i] * z[i], z[i], z[i]));
+            break;
+        case ACT_SILU:
+#pragma unroll
+            for (int i = 0; i < V; ++i) z[i] = sigmoid_times(z[i], z[i]);
+            break;
+        default: break;
+    }
+}
+
+__device__ __forceinline__ float load_out(const char* p, int dt) {
+    if (dt == DT_F32) return *reinterpret_cast<const float*>(p);
+    const uint16_t u = *reinterpret_cast<const uint16_t*>(p);
+    return dt == DT_BF16 ? Elem<DT_BF16>::to_f32(u) : (float)__builtin_bit_cast(_Float16, u);
+}
+
+__device__ __forceinline__ uint16_t round_half(float f, int dt) {
+    return dt == DT_BF16 ? __builtin_bit_cast(uint16_t, (__bf16)f) : __builtin_bit_cast(uint16_t, (_Float16)f);
+}
+
+__device__ __forceinline__ void store_out(char* p, int dt, float v) {
+    if (dt == DT_F32)
+        *reinterpret_cast<float*>(p) = v;
+    else
+        *reinterpret_cast<uint16_t*>(p) = round_half(v, dt);
+}
+
+// V neighbouring elements from a column that is a multiple of V: rows are
+// 16-byte aligned, so this is too, or to all its bytes where they are fewer.
+template <int V>
+__device__ __forceinline__ void load_out_vec(const char* p, int dt, float (&f)[V]) {
+    if (dt == DT_F32) {
+        __builtin_memcpy(f, __builtin_assume_aligned(p, V * 4 < 16 ? V * 4 : 16), V * 4);
+    } else {
+        uint16_t u[V];
+        __builtin_memcpy(u, __builtin_assume_aligned(p, V * 2 < 16 ? V * 2 : 16), V * 2);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            f[i] = dt == DT_BF16 ? Elem<DT_BF16>::to_f32(u[i]) : (float)__builtin_bit_cast(_Float16, u[i]);
+    }
+}
+
+template <int V>
+__device__ __forceinline__ void store_out_vec(char* p, int dt, const float (&f)[V]) {
+    if (dt == DT_F32) {
+        __builtin_memcpy(__builtin_assume_aligned(p, V * 4 < 16 ? V * 4 : 16), f, V * 4);
+    } else {
+        uint16_t u[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) u[i] = round_half(f[i], dt);
+        __builtin_memcpy(__builtin_assume_aligned(p, V * 2 < 16 ? V * 2 : 16), u, V * 2);
+    }
+}
+
+// What finishing V neighbouring results of row m from column n reads beside
+// them: gate (1 without one), residual (0) and the row's scale, loaded ahead.
+template <int V>
+struct Side {
+    float g[V], r[V], xs;
+    __device__ __forceinline__ void load(const LinearParams& p, int m, int n) {
+        const int oes = p.out_dt == DT_F32 ? 4 : 2;
+        const bool in = m < p.M && n < p.N, vec = p.vec && n + V <= p.N;
+        xs = p.xs && in && p.S == 1 ? p.xs[m] : 1.0f;
+        get(p.gate, m * p.ldg + (long long)n * oes, p, n, in, vec, 1.0f, g);
+        get(p.res, m * p.ldr + (long long)n * oes, p, n, in, vec, 0.0f, r);
+    }
+    __device__ __forceinline__ void get(const char* base, long long at, const LinearParams& p, int n, bool in, bool vec,
+                                        float none, float (&f)[V]) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = none;
+        if (!base || !in || p.S > 1) return;
+        if (vec) {
+            load_out_vec<V>(base + at, p.out_dt, f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (n + i < p.N) f[i] = load_out(base + at + i * (p.out_dt == DT_F32 ? 4 : 2), p.out_dt);
+        }
+    }
+};
+
+// Finish V neighbouring results of row m from column n, whose column scales
+// and bias values are cs and cb: the one rounding to y's type is the last step.
+template <int V>
+__device__ __forceinline__ void finish(const LinearParams& p, int m, int n, const float (&acc)[V], const float (&cs)[V],
+                                       const float (&cb)[V], const Side<V>& side) {
+    if (m >= p.M || n >= p.N) return;
+    const int oes = p.out_dt == DT_F32 ? 4 : 2;
+    char* y = p.y + m * p.ldy + (long long)n * oes;
+    float v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = acc[i] * side.xs * cs[i] + cb[i];
+    activate<V>(v, p.act);
+    if (p.gate) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] *= side.g[i];
+    }
+    if (p.res) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] += side.r[i];
+    }
+    if (p.vec && n + V <= p.N) {
+        store_out_vec<V>(y, p.out_dt, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (n + i < p.N) store_out(y + i * oes, p.out_dt, v[i]);
+    }
+}
+
+// Partial sums of a split reduction: [S][M][N] floats.
+template <int V>
+__device__ __forceinline__ void store_part(const LinearParams& p, int split, int m, int n, const float (&v)[V]) {
+    if (m >= p.M || n >= p.N) return;
+    float* o = p.part + ((long long)split * p.M + m) * p.N + n;
+    if (n + V <= p.N) {
+        __builtin_memcpy(o, v, V * 4);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (n + i < p.N) o[i] = v[i];
+    }
+}
+
+// Column values of V neighbours from n: scales and bias.
+template <int V>
+__device__ __forceinline__ void column_values(const LinearParams& p, int n, float (&s)[V], float (&b)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        s[i] = p.ws && n + i < p.N ? p.ws[n + i] : 1.0f;
+        b[i] = p.bias && n + i < p.N ? p.bias[n + i] : 0.0f;
+    }
+}
+
+// A chunk of a row from byte k of it (zeros from byte kbytes on), at any
+// alignment: gfx950 takes a 16-byte global load at any address.
+template <int ES>
+__device__ __forceinline__ uint4v load_chunk(const char* row, long long k, int kbytes) {
+    uint4v v = {0, 0, 0, 0};
+    const long long left = kbytes - k;
+    if (left >= 16) {
+        __builtin_memcpy(&v, row + k, 16);
+    } else if (left > 0) {
+#pragma unroll
+        for (int i = 0; i < 16 / ES; ++i) {
+            if (i * ES >= left) continue;
+            unsigned e;
+            if constexpr (ES == 4)
+                e = reinterpret_cast<const uint32_t*>(row + k)[i];
+            else if constexpr (ES == 2)
+                e = reinterpret_cast<const uint16_t*>(row + k)[i];
+            else
+                e = reinterpret_cast<const uint8_t*>(row + k)[i];
+            v[i * ES / 4] |= e << (8 * (i * ES % 4));
+        }
+    }
+    return v;
+}
+
+// -------------------------------------------------------------- row form --
+// Few rows of x (MF groups of 16).  Bound by reading the weights once.  A
+// workgroup takes 16 rows of w; its waves share the reduction, wave v taking
+// every NW-th stage, and lanes load both operands straight to registers in
+// the order the 16 x 16 instruction takes them (chunks l / 16 and 4 + l / 16
+// of row l % 16's 128 bytes), so every load of w is used once and nothing
+// passes through LDS before the waves' sums are joined there.
+constexpr int kRowWaves = 8;
+
+template <int DT, int MF>
+__global__ __launch_bounds__(kRowWaves * 64) void linear_rows_kernel(LinearParams p) {
+    constexpr int ES = elem_size<DT>();
+    constexpr int U = MF == 1 ? 4 : 2;  // stages in flight
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n0 = blockIdx.x * 16;
+    const int lr = lane & 15, lg = lane >> 4;
+    const int wr = n0 + lr < p.N ? n0 + lr : p.N - 1;
+    const char* w = p.w + wr * p.ldw;
+    const char* x[MF];
+#pragma unroll
+    for (int f = 0; f < MF; ++f) {
+        const int m = f * 16 + lr;
+        x[f] = p.x + (m < p.M ? m : p.M - 1) * p.ldx;
+    }
+    floatx4 acc[MF] = {};
+    const int stages = (p.kbytes + kStage - 1) / kStage;
+    for (int st0 = wave; st0 < stages; st0 += kRowWaves * U) {
+        uint4v a[U][2], b[U][MF][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long k = (long long)(st0 + u * kRowWaves) * kStage + lg * 16;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                a[u][h] = load_chunk<ES>(w, k + h * 64, p.kbytes);
+#pragma unroll
+                for (int f = 0; f < MF; ++f) b[u][f][h] = load_chunk<ES>(x[f], k + h * 64, p.kbytes);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int f = 0; f < MF; ++f) acc[f] = mma16<DT>(a[u][0], a[u][1], b[u][f][0], b[u][f][1], acc[f]);
+    }
+    // join the waves' sums: results [row of x][row of w], wave after wave
+    __shared__ __align__(16) float red[kRowWaves][MF * 256];
+#pragma unroll
+    for (int f = 0; f < MF; ++f)
+        *reinterpret_cast<floatx4*>(&red[wave][f * 256 + lr * 16 + lg * 4]) = acc[f];
+    __syncthreads();
+    for (int o = threadIdx.x; o < MF * 256; o += kRowWaves * 64) {
+        const int m = o >> 4, n = n0 + (o & 15);
+        if (m >= p.M || n >= p.N) continue;
+        float v[1] = {0.0f}, s[1], b[1];
+#pragma unroll
+        for (int i = 0; i < kRowWaves; ++i) v[0] += red[i][o];
+        column_values<1>(p, n, s, b);
+        Side<1> side;
+        side.load(p, m, n);
+        finish<1>(p, m, n, v, s, b, side);
+    }
+}
+
+// ------------------------------------------------------------- tile form --
+// BM x BN results a workgroup (rows of x, rows of w), WM x WN waves of
+// 32 MF x 32 NF each, on 32 x 32 instructions.  A stage (128 bytes of each of
+// the tile's rows) goes to one of two LDS buffers; a wave reads its operands
+// half a stage (64 bytes) ahead of the instructions that use them:
+//
+//   read half 1 of stage t | instructions on half 0 | wait for stage t + 1, barrier
+//   start loading stage t + 2 | read half 0 of stage t + 1 | instructions on half 1
+//
+// so every LDS read has half a stage of matrix instructions to arrive, every
+// load a whole stage, and one barrier a stage both ends the reads of a buffer
+// and publishes the next one.
+//
+// LDS banks: a cycle serves 16 lanes of a 16-byte read from 64 banks (two
+// 128-byte rows).  Chunk c of a row is stored at c ^ f(row), f giving the 8
+// rows of equal parity among the 16 that are read together 8 different places:
+// f = (row / 2) % 8 for x; for w, whose instruction rows 8 q + 4 h + i are its
+// rows 16 h + 4 q + i of each 32 (a lane of half h then holds 16 neighbours),
+// f = 4 (row / 16 % 2) + 2 (row / 4 % 2) + row / 2 % 2.
+__device__ __forceinline__ int rot_x(int row) { return (row >> 1) & 7; }
+__device__ __forceinline__ int rot_w(int row) { return ((row >> 2) & 4) | ((row >> 1) & 2) | ((row >> 1) & 1); }
+
+// 16 bytes a lane from base + off (zeros where off is kBufOut or above) to the
+// wave's 1024 bytes of LDS at `to`; base and `to` are wave-uniform.
+__device__ __forceinline__ void load_to_lds(const char* base, unsigned off, char* to) {
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, 0x7fffffff, kBufRaw);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)to, 16, off, 0, 0, 0);
+}
+
+// The tile of workgroup b: XCD b % 8 takes one run of tiles, ordered in bands
+// of 8 row tiles, so that what runs at one time on an XCD shares its L2.
+__device__ __forceinline__ void tile_of(const LinearParams& p, int& tm, int& tn, int& split) {
+    const unsigned tiles = (unsigned)p.tiles_m * p.tiles_n, nb = tiles * p.S;
+    const unsigned xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
+    const unsigned q = nb >> 3, r = nb & 7;
+    const unsigned id = xcd * q + (xcd < r ? xcd : r) + idx;
+    split = id / tiles;
+    const unsigned t = id - split * tiles;
+    const unsigned band = 8u * p.tiles_n;
+    const unsigned b = t / band, in = t - b * band;
+    const unsigned rows = (unsigned)p.tiles_m - b * 8 < 8 ? p.tiles_m - b * 8 : 8;
+    tn = in / rows;
+    tm = b * 8 + (in - tn * rows);
+}
+
+// The results' way through LDS (the end of the kernel): floats between the
+// rows of a wave's area (the vectors of 16 lanes in different banks), groups of
+// 32 rows it holds, and the bytes a workgroup needs for that or the stages.
+template <int NF> constexpr int row_stride() { return 32 * NF + 4; }
+template <int MF> constexpr int turn_groups() { return MF < 2 ? MF : 2; }
+template <int WM, int WN, int MF, int NF>
+constexpr int tile_lds() {
+    const int stages = 2 * (WM * MF + WN * NF) * 32 * kStage;
+    const int turn = WM * WN * turn_groups<MF>() * 32 * row_stride<NF>() * 4;
+    return stages > turn ? stages : turn;
+}
+
+template <int DT, int WM, int WN, int MF, int NF, bool AL>
+__global__ __launch_bounds__(WM* WN * 64) void linear_tile_kernel(LinearParams p) {
+    constexpr int ES = elem_size<DT>();
+    constexpr int NW = WM * WN;
+    constexpr int BM = WM * MF * 32, BN = WN * NF * 32;
+    constexpr int XL = BM / 8 / NW, WL = BN / 8 / NW;  // 8-row loads of a wave
+    static_assert(XL * NW * 8 == BM && WL * NW * 8 == BN, "whole loads");
+    constexpr int BUF = (BM + BN) * kStage;
+    extern __shared__ __align__(16) char lds[];
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave % WM, wn = wave / WM;
+    int tm, tn, split;
+    tile_of(p, tm, tn, split);
+    const int m0 = tm * BM, n0 = tn * BN;
+    const int st0 = split * p.stages_per_split;
+    const int all = (p.kbytes + kStage - 1) / kStage;
+    const int stages = all - st0 < p.stages_per_split ? all - st0 : p.stages_per_split;
+
+    // ---- loads: a wave's load j fills rows (wave + NW j) * 8 .. + 7 of x's
+    // (then w's) part of a buffer, lane l place l % 8 of row l / 8.  Rows past
+    // the end are the last row again (their results are not stored).
+    const char* xb = p.x + m0 * p.ldx + (long long)st0 * kStage;
+    const char* wb = p.w + n0 * p.ldw + (long long)st0 * kStage;
+    // A lane's place is the same in all its loads (its rows differ by
+    // multiples of 32), so the chunk it loads is too: byte cx (cw) of the stage.
+    static_assert(NW % 4 == 0, "rows of one lane's loads differ by multiples of 32");
+    const int cx = ((lane & 7) ^ rot_x(wave * 8 + (lane >> 3))) << 4;
+    const int cw = ((lane & 7) ^ rot_w(wave * 8 + (lane >> 3))) << 4;
+    unsigned xo[XL], wo[WL];
+#pragma unroll
+    for (int j = 0; j < XL; ++j) {
+        const int row = (wave + NW * j) * 8 + (lane >> 3);
+        xo[j] = (unsigned)((m0 + row < p.M ? row : p.M - 1 - m0) * (int)p.ldx);
+    }
+#pragma unroll
+    for (int j = 0; j < WL; ++j) {
+        const int row = (wave + NW * j) * 8 + (lane >> 3);
+        wo[j] = (unsigned)((n0 + row < p.N ? row : p.N - 1 - n0) * (int)p.ldw);
+    }
+    if constexpr (AL) {
+#pragma unroll
+        for (int j = 0; j < XL; ++j) xo[j] += cx;
+#pragma unroll
+        for (int j = 0; j < WL; ++j) wo[j] += cw;
+    }
+    uint4v xr[AL ? 1 : XL], wr[AL ? 1 : WL];  // unaligned rows pass through registers
+
+    auto start_loads = [&](int st, int buf) {
+        const char* xs = xb + (long long)st * kStage;
+        const char* ws = wb + (long long)st * kStage;
+        const int left = p.kbytes - (st0 + st) * kStage;  // bytes of the rows from this stage on
+        if constexpr (AL) {
+            char* base = lds + buf * BUF + wave * 1024;
+            // past the rows' end a lane loads zeros
+            const unsigned xend = cx >= left ? kBufOut : 0, wend = cw >= left ? kBufOut : 0;
+#pragma unroll
+            for (int j = 0; j < XL; ++j)
+                load_to_lds(xs, xo[j] | xend, base + j * NW * 1024);
+#pragma unroll
+            for (int j = 0; j < WL; ++j)
+                load_to_lds(ws, wo[j] | wend, base + BM * kStage + j * NW * 1024);
+        } else {
+#pragma unroll
+            for (int j = 0; j < XL; ++j) xr[j] = load_chunk<ES>(xs + xo[j], cx, left);
+#pragma unroll
+            for (int j = 0; j < WL; ++j) wr[j] = load_chunk<ES>(ws + wo[j], cw, left);
+        }
+    };
+    // the loads started last are in buffer buf once this and a barrier are passed
+    auto finish_loads = [&](int buf) {
+        if constexpr (!AL) {
+            char* base = lds + buf * BUF + wave * 1024 + lane * 16;
+#pragma unroll
+            for (int j = 0; j < XL; ++j) *reinterpret_cast<uint4v*>(base + j * NW * 1024) = xr[j];
+#pragma unroll
+            for (int j = 0; j < WL; ++j) *reinterpret_cast<uint4v*>(base + BM * kStage + j * NW * 1024) = wr[j];
+        }
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+
+    // ---- operand reads: half s of a stage, chunks 4 s + h and 4 s + 2 + h
+    const int lj = lane & 31, lh = lane >> 5;
+    const int wrow = 16 * ((lj >> 2) & 1) + 4 * (lj >> 3) + (lj & 3);
+    const int xa = (wm * MF * 32 + lj) * kStage + ((lh ^ rot_x(lj)) << 4);
+    const int wa = BM * kStage + (wn * NF * 32 + wrow) * kStage + ((lh ^ rot_w(wrow)) << 4);
+    struct Half {
+        uint4v x[MF][2], w[NF][2];
+    };
+    auto read_half = [&](Half& h, int buf, int s) {
+        const char* b = lds + buf * BUF;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int xor_ = s * 64 + c * 32;
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+                h.w[f][c] = *reinterpret_cast<const uint4v*>(b + (wa ^ xor_) + f * 32 * kStage);
+#pragma unroll
+            for (int f = 0; f < MF; ++f)
+                h.x[f][c] = *reinterpret_cast<const uint4v*>(b + (xa ^ xor_) + f * 32 * kStage);
+        }
+    };
+    floatx16 acc[MF][NF] = {};
+    auto products = [&](const Half& h) {
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+#pragma unroll
+            for (int j = 0; j < NF; ++j)
+                acc[i][j] = mma32<DT>(h.w[j][0], h.w[j][1], h.x[i][0], h.x[i][1], acc[i][j]);
+    };
+
+    Half h0, h1;
+    start_loads(0, 0);
+    finish_loads(0);
+    if (stages > 1) start_loads(1, 1);
+    read_half(h0, 0, 0);
+    for (int t = 0; t < stages - 1; ++t) {
+        const int buf = t & 1;
+        read_half(h1, buf, 1);
+        products(h0);
+        __builtin_amdgcn_sched_barrier(0);
+        finish_loads(buf ^ 1);
+        if (t + 2 < stages) start_loads(t + 2, buf);
+        __builtin_amdgcn_sched_barrier(0);
+        read_half(h0, buf ^ 1, 0);
+        products(h1);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    read_half(h1, (stages - 1) & 1, 1);
+    products(h0);
+    products(h1);
+
+    // ---- results.  Lane l holds, of tile (i, j), row l % 32 of x and the 16
+    // rows of w from 16 (l / 32).  Each wave turns its 32 rows of tiles (i, .)
+    // through LDS of its own, so that lanes hold 8 neighbours of a row and a
+    // row's lanes are neighbours too: whole 128-byte lines of y, gate and
+    // residual with NF = 2 and two-byte elements.
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();  // the buffers are free
+    asm volatile("" ::: "memory");
+    constexpr int RS = row_stride<NF>();
+    constexpr int LPR = 32 * NF / 8;      // lanes a row
+    constexpr int RPS = 64 / LPR;         // rows a step
+    constexpr int STEPS = 32 / RPS;       // steps a 32-row group
+    constexpr int GR = turn_groups<MF>();
+    float* area = reinterpret_cast<float*>(lds) + wave * GR * 32 * RS;
+    const int n = n0 + wn * NF * 32 + (lane % LPR) * 8;
+    float cs[8], cb[8];
+    if (p.S == 1) column_values<8>(p, n, cs, cb);
+#pragma unroll
+    for (int i0 = 0; i0 < MF; i0 += GR) {
+#pragma unroll
+        for (int i = 0; i < GR; ++i)
+#pragma unroll
+            for (int j = 0; j < NF; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; r += 4)
+                    *reinterpret_cast<floatx4*>(area + (i * 32 + lj) * RS + j * 32 + lh * 16 + r) =
+                        floatx4{acc[i0 + i][j][r], acc[i0 + i][j][r + 1], acc[i0 + i][j][r + 2], acc[i0 + i][j][r + 3]};
+        // a wave's LDS operations complete in order: no barrier
+#pragma unroll 1
+        for (int i = 0; i < GR; ++i) {
+            const int row = i * 32 + lane / LPR;
+            const int m = m0 + (wm * MF + i0) * 32 + row;
+            Side<8> side[STEPS];
+#pragma unroll
+            for (int t = 0; t < STEPS; ++t) side[t].load(p, m + t * RPS, n);
+#pragma unroll
+            for (int t = 0; t < STEPS; ++t) {
+                float v[8];
+                __builtin_memcpy(v, __builtin_assume_aligned(area + (row + t * RPS) * RS + (lane % LPR) * 8, 16), 32);
+                if (p.S > 1)
+                    store_part<8>(p, split, m + t * RPS, n, v);
+                else
+                    finish<8>(p, m + t * RPS, n, v, cs, cb, side[t]);
+            }
+        }
+        asm volatile("" ::: "memory");
+    }
+}
+
+// Join the parts of a split reduction, part after part, and finish.
+__global__ __launch_bounds__(256) void linear_join_kernel(LinearParams p) {
+    const int nv = (p.N + 3) / 4;
+    const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (id >= (long long)p.M * nv) return;
+    const int m = (int)(id / nv), n = (int)(id - (long long)m * nv) * 4;
+    const float* part = p.part + (long long)m * p.N + n;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s[4], b[4];
+    const int S = p.S;
+    p.S = 1;  // what is left is an unsplit product's epilogue
+    Side<4> side;
+    side.load(p, m, n);
+    for (int k = 0; k < S; ++k, part += (long long)p.M * p.N) {
+        if (n + 4 <= p.N) {
+            float f[4];
+            __builtin_memcpy(f, part, 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += f[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (n + i < p.N) v[i] += part[i];
+        }
+    }
+    column_values<4>(p, n, s, b);
+    finish<4>(p, m, n, v, s, b, side);
+}
+
+template <int DT, int WM, int WN, int MF, int NF, bool AL>
+hipError_t launch_tile(LinearParams p, int S, hipStream_t stream) {
+    constexpr int BM = WM * MF * 32, BN = WN * NF * 32;
+    constexpr int LDS = tile_lds<WM, WN, MF, NF>();
+    static_assert(LDS <= 160 * 1024, "one workgroup a CU at least");
+    p.tiles_m = (p.M + BM - 1) / BM;
+    p.tiles_n = (p.N + BN - 1) / BN;
+    const int stages = (p.kbytes + kStage - 1) / kStage;
+    p.S = S;
+    p.stages_per_split = (stages + S - 1) / S;
+    auto* kernel = linear_tile_kernel<DT, WM, WN, MF, NF, AL>;
+    static std::atomic<unsigned long long> lds_set{0};  // a bit per device
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(lds_set.load(std::memory_order_relaxed) & bit)) {
+        e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
+        if (e != hipSuccess) {
+            (void)hipGetLastError();
+            return e;
+        }
+        lds_set.fetch_or(bit, std::memory_order_relaxed);
+    }
+    (void)hipGetLastError();
+    kernel<<<dim3((unsigned)(p.tiles_m * p.tiles_n * p.S)), dim3(WM * WN * 64), LDS, stream>>>(p);
+    e = hipGetLastError();
+    if (e != hipSuccess || S == 1) return e;
+    const long long items = (long long)p.M * ((p.N + 3) / 4);
+    linear_join_kernel<<<dim3((unsigned)((items + 255) / 256)), dim3(256), 0, stream>>>(p);
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t launch_dt(const LinearPlan& plan, const LinearParams& p, bool aligned, hipStream_t stream) {
+    (void)hipGetLastError();
+    const dim3 rows_grid((unsigned)((p.N + 15) / 16)), rows_block(kRowWaves * 64);
+    constexpr int ROW_DT = DT == DT_E4M3 ? DT_E4M3_WIDE : DT;
+    switch (plan.form) {
+        case LIN_ROW16: linear_rows_kernel<ROW_DT, 1><<<rows_grid, rows_block, 0, stream>>>(p); return hipGetLastError();
+        case LIN_ROW32: linear_rows_kernel<ROW_DT, 2><<<rows_grid, rows_block, 0, stream>>>(p); return hipGetLastError();
+        case LIN_T64:
+            return aligned ? launch_tile<DT, 2, 2, 1, 1, true>(p, plan.S, stream)
+                           : launch_tile<DT, 2, 2, 1, 1, false>(p, plan.S, stream);
+        case LIN_T256:
+            if (aligned) return launch_tile<DT, 2, 4, 4, 2, true>(p, plan.S, stream);
+            return launch_tile<DT, 2, 2, 2, 2, false>(p, plan.S, stream);
+        default:
+            return aligned ? launch_tile<DT, 2, 2, 2, 2, true>(p, plan.S, stream)
+                           : launch_tile<DT, 2, 2, 2, 2, false>(p, plan.S, stream);
+    }
+}
+
+}  // namespace
+
+LinearPlan linear_plan(int M, int N, int kbytes, int dtype) {
+    if (M <= 16) return {LIN_ROW16, 1};
+    if (M <= 32) return {LIN_ROW32, 1};
+    const auto tiles = [&](int b) { return (long long)((M + b - 1) / b) * ((N + b - 1) / b); };
+    if (tiles(256) >= 256) return {LIN_T256, 1};
+    if (tiles(128) >= 256) return {LIN_T128, 1};
+    const long long t = tiles(64);
+    const int stages = (kbytes + kStage - 1) / kStage;
+    int S = 1;
+    while (t * S < 256 && S < 16 && stages / (S * 2) >= 4) S *= 2;
+    // every part has stages of its own
+    const int per = (stages + S - 1) / S;
+    return {LIN_T64, (stages + per - 1) / per};
+}
+
+hipError_t launch_linear(const LinearPlan& plan, LinearParams p, int dtype, bool aligned, hipStream_t stream) {
+    switch (dtype) {
+        case DT_F32: return launch_dt<DT_F32>(plan, p, aligned, stream);
+        case DT_F16: return launch_dt<DT_F16>(plan, p, aligned, stream);
+        case DT_BF16: return launch_dt<DT_BF16>(plan, p, aligned, stream);
+        default:
+            return p.out_dt == DT_F32 ? launch_dt<DT_E4M3_WIDE>(plan, p, aligned, stream)
+                                      : launch_dt<DT_E4M3>(plan, p, aligned, stream);
+    }
+}
+
+}  // namespace ct

@@ -1,0 +1,329 @@
+// Row operators: the root-mean-square norm with the residual's addition, and
+// the 8-bit quantization of rows.
+//
+//   h = x + residual                      (fp32; stored rounded to x's type)
+//   y = h * r * gain,  r = 1 / sqrt(mean h^2 + eps)      (norm; else y = h)
+//   e4m3:  a = max(max |y|, 2^-100),  scale = a / 448,  q = rne(y / scale)
+//
+// The row factor r cancels out of q: y / scale = t * 448 / max |t| with
+// t = h * gain.  So the sum of squares and the maximum of |t| are reduced
+// together, over one reading of the row, which stays in registers, and q
+// takes two roundings of 32 bits (t, and its product with 448 / max |t|)
+// before its own.  The quotient form y = t * r, q = y * (448 / a) is kept
+// for the rows where 448 / max |t| could leave the range of fp32 (a or
+// max |t| below 2^-100, or not finite).
+//
+// The maximum is taken over the bit patterns of |t| as unsigned integers:
+// the order is that of the values, infinity above every finite value and NaN
+// above infinity, so a NaN anywhere in a row reaches its scale.
+//
+// Bound by memory: about 5 operations an element.  A row is held by TPR
+// threads, 16 bytes of the input's type a load and C loads a thread, all
+// issued before the first is used.
+#include "ct_device.hpp"
+#include "block_kernels.hpp"
+
+namespace ct {
+
+namespace {
+
+constexpr float kE4m3Max = 448.0f;
+constexpr float kFloor = 0x1p-100f;
+
+enum { OUT_E4M3 = 3 };  // out_dt beyond DT_F32, DT_F16, DT_BF16
+
+// n elements of type DT at p (n < V: the row's end) as floats, zeros beyond.
+// A whole vector is one 16-byte load at whatever alignment the row has: gfx950
+// takes global accesses at any byte address.
+template <int DT> struct Vec;
+template <> struct Vec<DT_F32> { static constexpr int V = 4; };
+template <> struct Vec<DT_F16> { static constexpr int V = 8; };
+template <> struct Vec<DT_BF16> { static constexpr int V = 8; };
+
+template <int DT, int V>
+__device__ __forceinline__ void load_vec(const char* p, int n, float (&f)[V]) {
+    using T = typename Elem<DT>::T;
+    T v[V];
+    if (n >= V) {
+        __builtin_memcpy(v, p, sizeof(v));
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            v[i] = T(0);
+            if (i < n) v[i] = reinterpret_cast<const T*>(p)[i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = Elem<DT>::to_f32(v[i]);
+}
+
+__device__ __forceinline__ uint16_t to_bf16(float f) {
+    // round to nearest even; a NaN stays one
+    return __builtin_bit_cast(uint16_t, (__bf16)f);
+}
+
+template <int V, typename T>
+__device__ __forceinline__ void store_elems(char* p, int n, const T (&v)[V]) {
+    if (n >= V) {
+        __builtin_memcpy(p, v, sizeof(v));
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i < n) reinterpret_cast<T*>(p)[i] = v[i];
+    }
+}
+
+template <int V>
+__device__ __forceinline__ void store_vec(char* p, int n, int dt, const float (&f)[V]) {
+    if (dt == DT_F32) {
+        store_elems<V, float>(p, n, f);
+    } else {
+        uint16_t v[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            v[i] = dt == DT_BF16 ? to_bf16(f[i]) : __builtin_bit_cast(uint16_t, (_Float16)f[i]);
+        store_elems<V, uint16_t>(p, n, v);
+    }
+}
+
+// V values to e4m3 (round to nearest even).
+template <int V>
+__device__ __forceinline__ void store_e4m3(char* p, int n, const float (&f)[V]) {
+    uint8_t b[V];
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+        int u = __builtin_amdgcn_cvt_pk_fp8_f32(f[i], f[i + 1], 0, false);
+        u = __builtin_amdgcn_cvt_pk_fp8_f32(f[i + 2], f[i + 3], u, true);
+        __builtin_memcpy(b + i, &u, 4);
+    }
+    store_elems<V, uint8_t>(p, n, b);
+}
+
+__device__ __forceinline__ int elem_bytes(int dt) { return dt == DT_F32 ? 4 : dt == OUT_E4M3 ? 1 : 2; }
+
+// What a row's statistics give: every element is (t * m1) * m2.
+struct RowFactors {
+    float m1, m2;
+};
+
+// ss: the sum of squares, tbits: the bits of max |t|.
+template <bool NORM>
+__device__ __forceinline__ RowFactors row_factors(float ss, uint32_t tbits, int D, int out_dt, float eps, float* scale) {
+    const float r = NORM ? 1.0f / sqrtf(ss / (float)D + eps) : 1.0f;
+    if (out_dt != OUT_E4M3) return {r, 1.0f};
+    const float tmax = __uint_as_float(tbits);
+    const float a0 = r * tmax;
+    const float a = a0 < kFloor ? kFloor : a0;  // NaN stays
+    if (scale) *scale = a / kE4m3Max;
+    if (tmax >= kFloor && a0 >= kFloor) return {kE4m3Max / tmax, 1.0f};
+    return {r, kE4m3Max / a};
+}
+
+// Reductions over the TPR threads of a row (whole waves): the sum of squares
+// and the maximum, every thread getting both.
+template <int TPR>
+__device__ __forceinline__ void reduce_row(float& ss, uint32_t& tb) {
+#pragma unroll
+    for (int o = 32; o; o >>= 1) {
+        ss += __shfl_xor(ss, o);
+        const uint32_t u = __shfl_xor(tb, o);
+        tb = u > tb ? u : tb;
+    }
+    if constexpr (TPR > 64) {
+        constexpr int W = TPR / 64;
+        __shared__ float s_ss[W];
+        __shared__ uint32_t s_tb[W];
+        if ((threadIdx.x & 63) == 0) {
+            s_ss[threadIdx.x >> 6] = ss;
+            s_tb[threadIdx.x >> 6] = tb;
+        }
+        __syncthreads();
+        ss = 0.0f;
+        tb = 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            ss += s_ss[w];
+            tb = s_tb[w] > tb ? s_tb[w] : tb;
+        }
+    }
+}
+
+// One row by TPR threads, in registers: D <= TPR * C * V.
+template <int DT, int TPR, int C, bool NORM>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rows_kernel(RowsParams p, int M) {
+    constexpr int V = Vec<DT>::V;
+    constexpr int RPB = TPR < 256 ? 256 / TPR : 1;  // rows a workgroup
+    const int lt = RPB > 1 ? threadIdx.x % TPR : threadIdx.x;
+    const long long row = (long long)blockIdx.x * RPB + (RPB > 1 ? threadIdx.x / TPR : 0);
+    if (row >= M) return;  // whole waves, and no barrier where a workgroup has several rows
+    const char* x = p.x + row * p.ldx;
+    constexpr int ES = sizeof(typename Elem<DT>::T);
+
+    float h[C][V];
+    uint32_t tb = 0;
+    float ss = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int e = (c * TPR + lt) * V;
+        load_vec<DT, V>(x + (long long)e * ES, p.D - e, h[c]);
+    }
+    if (p.res) {
+        const char* res = p.res + row * p.ldres;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int e = (c * TPR + lt) * V;
+            float f[V];
+            load_vec<DT, V>(res + (long long)e * ES, p.D - e, f);
+#pragma unroll
+            for (int i = 0; i < V; ++i) h[c][i] += f[i];
+        }
+    }
+    if (p.h) {
+        char* ho = p.h + row * p.ldh;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int e = (c * TPR + lt) * V;
+            store_vec<V>(ho + (long long)e * ES, p.D - e, DT, h[c]);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int e = (c * TPR + lt) * V;
+        if constexpr (NORM) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) ss = fmaf(h[c][i], h[c][i], ss);
+            if (p.gain) {
+                float g[V];
+                load_vec<DT_F32, V>(reinterpret_cast<const char*>(p.gain + e), p.D - e, g);
+#pragma unroll
+                for (int i = 0; i < V; ++i) h[c][i] *= g[i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint32_t u = __float_as_uint(h[c][i]) & 0x7fffffffu;
+            tb = u > tb ? u : tb;
+        }
+    }
+    reduce_row<TPR>(ss, tb);
+    const RowFactors f = row_factors<NORM>(ss, tb, p.D, p.out_dt, p.eps, lt == 0 && p.scale ? p.scale + row : nullptr);
+    char* y = p.y + row * p.ldy;
+    const int oes = elem_bytes(p.out_dt);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int e = (c * TPR + lt) * V;
+        float o[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = h[c][i] * f.m1 * f.m2;
+        char* yo = y + (long long)e * oes;
+        if (p.out_dt == OUT_E4M3)
+            store_e4m3<V>(yo, p.D - e, o);
+        else
+            store_vec<V>(yo, p.D - e, p.out_dt, o);
+    }
+}
+
+// A row of any length, read twice: statistics, then outputs.  h is written in
+// the second reading, after the elements it may replace.
+template <int DT, bool NORM>
+__global__ __launch_bounds__(1024) void rows_long_kernel(RowsParams p) {
+    constexpr int V = Vec<DT>::V, TPR = 1024;
+    constexpr int ES = sizeof(typename Elem<DT>::T);
+    const long long row = blockIdx.x;
+    const char* x = p.x + row * p.ldx;
+    const char* res = p.res ? p.res + row * p.ldres : nullptr;
+    float ss = 0.0f;
+    uint32_t tb = 0;
+    auto load_h = [&](long long e, float (&h)[V]) {
+        const int n = (int)((long long)p.D - e < V ? (long long)p.D - e : V);
+        load_vec<DT, V>(x + e * ES, n, h);
+        if (res) {
+            float f[V];
+            load_vec<DT, V>(res + e * ES, n, f);
+#pragma unroll
+            for (int i = 0; i < V; ++i) h[i] += f[i];
+        }
+    };
+    auto times_gain = [&](long long e, float (&h)[V]) {
+        if (!NORM || !p.gain) return;
+        const int n = (int)((long long)p.D - e < V ? (long long)p.D - e : V);
+        float g[V];
+        load_vec<DT_F32, V>(reinterpret_cast<const char*>(p.gain + e), n, g);
+#pragma unroll
+        for (int i = 0; i < V; ++i) h[i] *= g[i];
+    };
+    for (long long e = (long long)threadIdx.x * V; e < p.D; e += TPR * V) {
+        float h[V];
+        load_h(e, h);
+        if constexpr (NORM) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) ss = fmaf(h[i], h[i], ss);
+        }
+        times_gain(e, h);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint32_t u = __float_as_uint(h[i]) & 0x7fffffffu;
+            tb = u > tb ? u : tb;
+        }
+    }
+    reduce_row<TPR>(ss, tb);
+    const RowFactors f =
+        row_factors<NORM>(ss, tb, p.D, p.out_dt, p.eps, threadIdx.x == 0 && p.scale ? p.scale + row : nullptr);
+    char* y = p.y + row * p.ldy;
+    const int oes = elem_bytes(p.out_dt);
+    for (long long e = (long long)threadIdx.x * V; e < p.D; e += TPR * V) {
+        const int n = (int)((long long)p.D - e < V ? (long long)p.D - e : V);
+        float h[V], o[V];
+        load_h(e, h);
+        if (p.h) store_vec<V>(p.h + row * p.ldh + e * ES, n, DT, h);
+        times_gain(e, h);
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = h[i] * f.m1 * f.m2;
+        if (p.out_dt == OUT_E4M3)
+            store_e4m3<V>(y + e * oes, n, o);
+        else
+            store_vec<V>(y + e * oes, n, p.out_dt, o);
+    }
+}
+
+template <int DT, int TPR, int C>
+hipError_t launch_one(const RowsParams& p, int M, bool norm, hipStream_t stream) {
+    constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+    const dim3 grid((unsigned)(((long long)M + RPB - 1) / RPB)), block(TPR < 256 ? 256 : TPR);
+    if (norm)
+        rows_kernel<DT, TPR, C, true><<<grid, block, 0, stream>>>(p, M);
+    else
+        rows_kernel<DT, TPR, C, false><<<grid, block, 0, stream>>>(p, M);
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t launch_dt(const RowsParams& p, int M, bool norm, hipStream_t stream) {
+    constexpr int V = Vec<DT>::V;
+    const int D = p.D;
+    if (D <= 64 * V) return launch_one<DT, 64, 1>(p, M, norm, stream);
+    if (D <= 64 * V * 2) return launch_one<DT, 64, 2>(p, M, norm, stream);
+    if (D <= 256 * V) return launch_one<DT, 256, 1>(p, M, norm, stream);
+    if (D <= 256 * V * 2) return launch_one<DT, 256, 2>(p, M, norm, stream);
+    if (D <= 256 * V * 4) return launch_one<DT, 256, 4>(p, M, norm, stream);
+    if (D <= 1024 * V * 2) return launch_one<DT, 1024, 2>(p, M, norm, stream);
+    if (D <= 1024 * V * 4) return launch_one<DT, 1024, 4>(p, M, norm, stream);
+    if (norm)
+        rows_long_kernel<DT, true><<<dim3((unsigned)M), dim3(1024), 0, stream>>>(p);
+    else
+        rows_long_kernel<DT, false><<<dim3((unsigned)M), dim3(1024), 0, stream>>>(p);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rows(const RowsParams& p, int M, int dtype, bool norm, hipStream_t stream) {
+    (void)hipGetLastError();
+    switch (dtype) {
+        case DT_F32: return launch_dt<DT_F32>(p, M, norm, stream);
+        case DT_F16: return launch_dt<DT_F16>(p, M, norm, stream);
+        default: return launch_dt<DT_BF16>(p, M, norm, stream);
+    }
+}
+
+}  // namespace ct

@@ -55,6 +55,8 @@ constexpr int kSpaceVersion = 1;
 // ---------------------------------------------------------------- errors --
 thread_local char g_last_error[512] = "";
 
+}  // namespace
+
 int fail(int status, const char* fmt, ...) {
     va_list ap;
     va_start(ap, fmt);
@@ -66,6 +68,8 @@ int fail(int status, const char* fmt, ...) {
 int hip_fail(hipError_t e, const char* what) {
     return fail(CT_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
+
+namespace {
 
 bool log_debug() {
     static int v = -1;
