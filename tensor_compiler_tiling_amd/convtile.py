@@ -10,6 +10,7 @@ the library is missing, loading it raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import List, Optional, Tuple
 
@@ -645,59 +646,90 @@ def conv2d_depthwise(x, w, stride: int = 1, pad: int = 0, epilogue: int = CT_EPI
 
 
 # ---- transformer-block rows: matrices whose rows may lie apart -------------
-def _matrix(name: str, t, device, dtype=None, shape=None) -> int:
-    """Check a matrix argument; the distance between its rows, in elements."""
+# The smallest calls take a few microseconds on the device, less than a careless
+# wrapper takes on the host: what these helpers need of torch is looked up once,
+# and a well-formed argument passes its checks in one comparison.
+class _TorchSide:
+    def __init__(self):
+        import torch
+        self.empty, self.Tensor = torch.empty_strided, torch.Tensor  # the form that parses fastest
+        self.f32, self.bf16, self.e4m3 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
+        self.uint8 = torch.uint8
+        self.codes = {torch.float32: CT_F32, torch.float16: CT_F16, torch.bfloat16: CT_BF16}
+        self.current_device = torch.cuda.current_device
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.stream = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+_torch_side: Optional[_TorchSide] = None
+
+
+def _side() -> _TorchSide:
+    global _torch_side
+    if _torch_side is None:
+        _torch_side = _TorchSide()
+    return _torch_side
+
+
+def _refuse_matrix(name: str, t, device, dtype, M, D):
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions")
-    if t.device != device or not t.is_cuda:
+    if not t.is_cuda or t.device != device:
         raise ValueError(f"{name} must be a GPU tensor on the device of the others")
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    rows, cols = t.shape
-    if shape is not None and (rows, cols) != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {[rows, cols]}")
-    ld, step = t.stride()
-    if step != 1 and cols > 1:
+    if tuple(t.shape) != (M, D):
+        raise ValueError(f"{name} must be {[M, D]}, got {list(t.shape)}")
+    if D > 1 and t.stride(1) != 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    if rows <= 1:
-        return cols  # a single row has no stride to speak of
-    if ld < cols:
-        raise ValueError(f"{name}: rows must not overlap")
-    return ld
+    raise ValueError(f"{name}: rows must not overlap")
+
+
+def _matrix(name: str, t, device, dtype, M: int, D: int) -> int:
+    """Check a matrix argument; the distance between its rows, in elements."""
+    if t.shape == (M, D) and t.dtype is dtype and t.device == device:
+        ld, step = t.stride()
+        if step == 1 or D <= 1:
+            if M <= 1:
+                return D  # a single row has no stride to speak of
+            if ld >= D:
+                return ld
+    return _refuse_matrix(name, t, device, dtype, M, D)
 
 
 def _vector(name: str, t, device, n: int) -> int:
     """Check an fp32 vector argument; its address."""
-    import torch
-    if t.device != device or not t.is_cuda:
+    if t.device != device:
         raise ValueError(f"{name} must be a GPU tensor on the device of the others")
-    if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.dtype is not _side().f32 or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be {n} contiguous fp32 values")
     return t.data_ptr()
 
 
-def _place(device, stream):
-    """(context, stream handle): the context makes `device` current and, with
-    an explicit stream, has torch allocate outputs and workspace for that
-    stream; None where nothing has to change."""
+def _rows_of(name: str, t):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return t.shape
+
+
+def _code(dtype) -> int:
+    code = _side().codes.get(dtype)
+    return dtype_code(dtype) if code is None else code
+
+
+def _elsewhere(device, stream):
+    """A context that makes `device` current and, with an explicit stream, has
+    torch allocate outputs and workspace for that stream."""
     import torch
     if stream is None:
-        if device.index == torch.cuda.current_device():
-            return None, torch.cuda.current_stream().cuda_stream
-        return torch.cuda.device(device), torch.cuda.current_stream(device).cuda_stream
+        return torch.cuda.device(device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
     if stream.device != device:
         raise ValueError("the stream belongs to another device than the tensors")
-    return torch.cuda.stream(stream), stream.cuda_stream
-
-
-def _placed(device, stream, call, *args):
-    ctx, handle = _place(device, stream)
-    if ctx is None:
-        return call(handle, *args)
-    with ctx:
-        return call(handle, *args)
+    return torch.cuda.stream(stream)
 
 
 def rmsnorm(x, gain=None, residual=None, eps: float = 1e-6, out_dtype=None, h=True, out=None, scale=None,
@@ -710,116 +742,144 @@ def rmsnorm(x, gain=None, residual=None, eps: float = 1e-6, out_dtype=None, h=Tr
     residual stream; None without a residual or with h=False; h may name the
     tensor to write, x and residual among them).  x, residual, h and out are
     [M, D] with contiguous rows; gain is fp32 [D]."""
-    import torch
-    device, dtype = x.device, dtype_code(x.dtype)
-    ldx = _matrix("x", x, device)
-    M, D = x.shape
-    gp = None if gain is None else _vector("gain", gain, device, D)
+    T = _side()
+    M, D = _rows_of("x", x)
+    device = x.device
+    if stream is not None or device.index != T.current_device():
+        with _elsewhere(device, stream):
+            return rmsnorm(x, gain, residual, eps, out_dtype, h, out, scale)
+    xt = x.dtype
+    dtype = _code(xt)
+    ldx = _matrix("x", x, device, xt, M, D)
+    gp = rp = hp = sp = None
     ldr = ldh = 0
+    if gain is not None:
+        gp = _vector("gain", gain, device, D)
+    if out_dtype is None:
+        out_dtype = xt if out is None else out.dtype
+    q8 = out_dtype is T.e4m3
+    code = CT_E4M3 if q8 else _code(out_dtype)
     if residual is not None:
-        ldr = _matrix("residual", residual, device, x.dtype, (M, D))
-    hout = h if isinstance(h, torch.Tensor) else None
-    if hout is not None:
-        if residual is None:
-            raise ValueError("h is the sum with a residual, and there is none")
-        ldh = _matrix("h", hout, device, x.dtype, (M, D))
-    out_dtype = out_dtype or (out.dtype if out is not None else x.dtype)
-    q8 = out_dtype == torch.float8_e4m3fn
-    code = CT_E4M3 if q8 else dtype_code(out_dtype)
-    if out is not None:
-        _matrix("out", out, device, out_dtype, (M, D))
-    if scale is not None:
-        if not q8:
-            raise ValueError("scale belongs to 8-bit output")
-        _vector("scale", scale, device, M)
-
-    def call(handle):
-        y = out if out is not None else torch.empty((M, D), dtype=out_dtype, device=device)
-        sc = scale if scale is not None or not q8 else torch.empty(M, dtype=torch.float32, device=device)
-        ho, ld = hout, ldh
-        if ho is None and residual is not None and h is True:
-            ho, ld = torch.empty((M, D), dtype=x.dtype, device=device), D
-        check(_load().ct_rmsnorm_fwd(
-            x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, gp,
-            None if ho is None else ho.data_ptr(), ld, y.data_ptr(), y.stride(0) if M > 1 else D,
-            None if sc is None else sc.data_ptr(), M, D, dtype, code, eps, handle), "rmsnorm")
-        return y, sc, ho
-
-    return _placed(device, stream, call)
+        ldr = _matrix("residual", residual, device, xt, M, D)
+        rp = residual.data_ptr()
+        if h is True:
+            h, ldh = T.empty((M, D), (D, 1), dtype=xt, device=device), D
+        elif h is not False and h is not None:
+            ldh = _matrix("h", h, device, xt, M, D)
+        else:
+            h = None
+        hp = None if h is None else h.data_ptr()
+    elif isinstance(h, T.Tensor):
+        raise ValueError("h is the sum with a residual, and there is none")
+    else:
+        h = None
+    if out is None:
+        out, ldy = T.empty((M, D), (D, 1), dtype=out_dtype, device=device), D
+    else:
+        ldy = _matrix("out", out, device, out_dtype, M, D)
+    if q8:
+        if scale is None:
+            scale = T.empty((M,), (1,), dtype=T.f32, device=device)
+            sp = scale.data_ptr()
+        else:
+            sp = _vector("scale", scale, device, M)
+    elif scale is not None:
+        raise ValueError("scale belongs to 8-bit output")
+    st = _load().ct_rmsnorm_fwd(x.data_ptr(), ldx, rp, ldr, gp, hp, ldh, out.data_ptr(), ldy, sp, M, D, dtype, code,
+                                eps, T.stream(device.index))
+    if st:
+        check(st, "rmsnorm")
+    return out, scale, h
 
 
 def quantize_rows(x, out=None, scale=None, stream=None):
     """The rows of x [M, D] in 8 bits: (q float8_e4m3fn [M, D], scale fp32 [M]),
     x ~ scale[:, None] * q."""
-    import torch
-    device, dtype = x.device, dtype_code(x.dtype)
-    ldx = _matrix("x", x, device)
-    M, D = x.shape
-    if out is not None:
-        _matrix("out", out, device, torch.float8_e4m3fn, (M, D))
-    if scale is not None:
-        _vector("scale", scale, device, M)
+    T = _side()
+    M, D = _rows_of("x", x)
+    device = x.device
+    if stream is not None or device.index != T.current_device():
+        with _elsewhere(device, stream):
+            return quantize_rows(x, out, scale)
+    dtype = _code(x.dtype)
+    ldx = _matrix("x", x, device, x.dtype, M, D)
+    if out is None:
+        out, ldq = T.empty((M, D), (D, 1), dtype=T.e4m3, device=device), D
+    else:
+        ldq = _matrix("out", out, device, T.e4m3, M, D)
+    if scale is None:
+        scale = T.empty((M,), (1,), dtype=T.f32, device=device)
+        sp = scale.data_ptr()
+    else:
+        sp = _vector("scale", scale, device, M)
+    st = _load().ct_quantize_rows(x.data_ptr(), ldx, out.data_ptr(), ldq, sp, M, D, dtype, T.stream(device.index))
+    if st:
+        check(st, "quantize_rows")
+    return out, scale
 
-    def call(handle):
-        q = out if out is not None else torch.empty((M, D), dtype=torch.float8_e4m3fn, device=device)
-        sc = scale if scale is not None else torch.empty(M, dtype=torch.float32, device=device)
-        check(_load().ct_quantize_rows(x.data_ptr(), ldx, q.data_ptr(), q.stride(0) if M > 1 else D, sc.data_ptr(),
-                                       M, D, dtype, handle), "quantize_rows")
-        return q, sc
 
-    return _placed(device, stream, call)
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(M: int, N: int, K: int, dtype: int) -> int:
+    return max(0, _load().ct_linear_workspace_bytes(M, N, K, dtype))
 
 
 def _product(x, xs, w, ws, bias, act, gate, residual, out_dtype, out, stream):
-    import torch
+    T = _side()
+    M, K = _rows_of("x", x)
     device = x.device
-    q8 = xs is not None
-    ldx = _matrix("x", x, device, torch.float8_e4m3fn if q8 else None)
-    ldw = _matrix("w", w, device, x.dtype)
-    M, K = x.shape
-    N, K2 = w.shape
+    if stream is not None or device.index != T.current_device():
+        with _elsewhere(device, stream):
+            return _product(x, xs, w, ws, bias, act, gate, residual, out_dtype, out, None)
+    N, K2 = _rows_of("w", w)
     if K != K2:
         raise ValueError(f"x has rows of {K} and w of {K2}")
-    dtype = CT_E4M3 if q8 else dtype_code(x.dtype)
-    if act not in ACTIVATIONS:
-        raise ValueError(f"unknown activation {act!r}: one of {', '.join(ACTIVATIONS)}")
-    if out is not None:
-        _matrix("out", out, device, out_dtype, (M, N))
-        out_dtype = out.dtype
-    elif out_dtype is None:
-        out_dtype = torch.bfloat16 if q8 else x.dtype
-    code = dtype_code(out_dtype)
-    epi = None
-    if act != "none" or bias is not None or gate is not None or residual is not None:
-        epi = ct_linear_epilogue(ACTIVATIONS[act])
-        if bias is not None:
-            epi.bias = _vector("bias", bias, device, N)
-        if gate is not None:
-            epi.ldg = _matrix("gate", gate, device, out_dtype, (M, N))
-            epi.gate = gate.data_ptr()
-        if residual is not None:
-            epi.ldr = _matrix("residual", residual, device, out_dtype, (M, N))
-            epi.residual = residual.data_ptr()
-    if q8:
+    xt = x.dtype
+    if xs is None:
+        dtype = _code(xt)
+    else:
+        dtype = CT_E4M3
         xsp, wsp = _vector("xs", xs, device, M), _vector("ws", ws, device, N)
-
-    def call(handle):
-        lib = _load()
-        y = out if out is not None else torch.empty((M, N), dtype=out_dtype, device=device)
-        ldy = y.stride(0) if M > 1 else N
-        need = lib.ct_linear_workspace_bytes(M, N, K, dtype)
-        space = None if need <= 0 else torch.empty(need, dtype=torch.uint8, device=device)
-        sp, ep = None if space is None else space.data_ptr(), None if epi is None else ctypes.addressof(epi)
-        if q8:
-            st = lib.ct_linear_q8_fwd(x.data_ptr(), ldx, xsp, w.data_ptr(), ldw, wsp, y.data_ptr(), ldy, M, N, K, code,
-                                      ep, sp, max(need, 0), handle)
-        else:
-            st = lib.ct_linear_fwd(x.data_ptr(), ldx, w.data_ptr(), ldw, y.data_ptr(), ldy, M, N, K, dtype, code, ep,
-                                   sp, max(need, 0), handle)
-        check(st, "linear_q8" if q8 else "linear")
-        return y
-
-    return _placed(device, stream, call)
+        xt = T.e4m3
+    ldx = _matrix("x", x, device, xt, M, K)
+    ldw = _matrix("w", w, device, xt, N, K)
+    a = ACTIVATIONS.get(act)
+    if a is None:
+        raise ValueError(f"unknown activation {act!r}: one of {', '.join(ACTIVATIONS)}")
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else xt if xs is None else T.bf16
+    code = _code(out_dtype)
+    ep = None
+    if a or bias is not None or gate is not None or residual is not None:
+        bp = gp = rp = None
+        ldg = ldr = 0
+        if bias is not None:
+            bp = _vector("bias", bias, device, N)
+        if gate is not None:
+            ldg = _matrix("gate", gate, device, out_dtype, M, N)
+            gp = gate.data_ptr()
+        if residual is not None:
+            ldr = _matrix("residual", residual, device, out_dtype, M, N)
+            rp = residual.data_ptr()
+        epi = ct_linear_epilogue(a, bp, gp, ldg, rp, ldr)
+        ep = ctypes.addressof(epi)
+    if out is None:
+        out, ldy = T.empty((M, N), (N, 1), dtype=out_dtype, device=device), N
+    else:
+        ldy = _matrix("out", out, device, out_dtype, M, N)
+    need = _workspace_bytes(M, N, K, dtype)
+    space = sp = None
+    if need:
+        space = T.empty((need,), (1,), dtype=T.uint8, device=device)
+        sp = space.data_ptr()
+    if xs is None:
+        st = _load().ct_linear_fwd(x.data_ptr(), ldx, w.data_ptr(), ldw, out.data_ptr(), ldy, M, N, K, dtype, code, ep,
+                                   sp, need, T.stream(device.index))
+    else:
+        st = _load().ct_linear_q8_fwd(x.data_ptr(), ldx, xsp, w.data_ptr(), ldw, wsp, out.data_ptr(), ldy, M, N, K,
+                                      code, ep, sp, need, T.stream(device.index))
+    if st:
+        check(st, "linear" if xs is None else "linear_q8")
+    return out
 
 
 def linear(x, w, bias=None, act: str = "none", gate=None, residual=None, out_dtype=None, out=None, stream=None):

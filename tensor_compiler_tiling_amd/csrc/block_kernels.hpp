@@ -25,7 +25,8 @@ struct LinearParams {
     int M, N;
     int kbytes;          // bytes of a row of x and w
     int act, out_dt;
-    int vec;             // y, gate and residual rows are 16-byte aligned
+    int vec;             // 1: y, gate and residual rows are 16-byte aligned; 2: and at most 1 MiB apart,
+                         // of two-byte elements
     int tiles_m, tiles_n;
     int S, stages_per_split;
 };

@@ -17,6 +17,7 @@
 #include "block_kernels.hpp"
 
 #include <atomic>
+#include <type_traits>
 
 namespace ct {
 
@@ -123,29 +124,34 @@ __device__ __forceinline__ float sigmoid_times(float z, float u) {
     return z * __builtin_amdgcn_rcpf(1.0f + dev_exp(-u));
 }
 
+template <int ACT>
+__device__ __forceinline__ float activated(float z) {
+    if constexpr (ACT == ACT_RELU) return z < 0.0f ? 0.0f : z;  // NaN stays
+    if constexpr (ACT == ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
+    // 0.5 (1 + tanh u) = 1 / (1 + exp(-2 u)), u = sqrt(2 / pi) (z + 0.044715 z^3)
+    if constexpr (ACT == ACT_GELU_TANH) return sigmoid_times(z, 1.5957691f * fmaf(0.044715f * z * z, z, z));
+    if constexpr (ACT == ACT_SILU) return sigmoid_times(z, z);
+    return z;
+}
+
+// f(a constant of the activation's value)
+template <typename F>
+__device__ __forceinline__ void with_activation(int act, F f) {
+    switch (act) {
+        case ACT_RELU: f(std::integral_constant<int, ACT_RELU>{}); break;
+        case ACT_GELU: f(std::integral_constant<int, ACT_GELU>{}); break;
+        case ACT_GELU_TANH: f(std::integral_constant<int, ACT_GELU_TANH>{}); break;
+        case ACT_SILU: f(std::integral_constant<int, ACT_SILU>{}); break;
+        default: f(std::integral_constant<int, ACT_NONE>{}); break;
+    }
+}
+
 template <int V>
 __device__ __forceinline__ void activate(float (&z)[V], int act) {
-    switch (act) {
-        case ACT_RELU:
+    with_activation(act, [&](auto a) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) z[i] = z[i] < 0.0f ? 0.0f : z[i];  // NaN stays
-            break;
-        case ACT_GELU:
-#pragma unroll
-            for (int i = 0; i < V; ++i) z[i] = 0.5f * z[i] * (1.0f + erff(z[i] * 0.70710678f));
-            break;
-        case ACT_GELU_TANH:
-            // 0.5 (1 + tanh u) = 1 / (1 + exp(-2 u)), u = sqrt(2 / pi) (z + 0.044715 z^3)
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                z[i] = sigmoid_times(z[i], 1.5957691f * fmaf(0.044715f * z[i] * z[i], z[i], z[i]));
-            break;
-        case ACT_SILU:
-#pragma unroll
-            for (int i = 0; i < V; ++i) z[i] = sigmoid_times(z[i], z[i]);
-            break;
-        default: break;
-    }
+        for (int i = 0; i < V; ++i) z[i] = activated<decltype(a)::value>(z[i]);
+    });
 }
 
 __device__ __forceinline__ float load_out(const char* p, int dt) {
@@ -266,9 +272,16 @@ __device__ __forceinline__ void store_part(const LinearParams& p, int split, int
 template <int V>
 __device__ __forceinline__ void column_values(const LinearParams& p, int n, float (&s)[V], float (&b)[V]) {
 #pragma unroll
+    for (int i = 0; i < V; ++i) s[i] = 1.0f, b[i] = 0.0f;
+    if (n + V <= p.N) {
+        if (p.ws) __builtin_memcpy(s, p.ws + n, V * 4);
+        if (p.bias) __builtin_memcpy(b, p.bias + n, V * 4);
+        return;
+    }
+#pragma unroll
     for (int i = 0; i < V; ++i) {
-        s[i] = p.ws && n + i < p.N ? p.ws[n + i] : 1.0f;
-        b[i] = p.bias && n + i < p.N ? p.bias[n + i] : 0.0f;
+        if (p.ws && n + i < p.N) s[i] = p.ws[n + i];
+        if (p.bias && n + i < p.N) b[i] = p.bias[n + i];
     }
 }
 
@@ -361,17 +374,23 @@ __global__ __launch_bounds__(kRowWaves * 64) void linear_rows_kernel(LinearParam
 }
 
 // ------------------------------------------------------------- tile form --
-// BM x BN results a workgroup (rows of x, rows of w), WM x WN waves of
-// 32 MF x 32 NF each, on 32 x 32 instructions.  A stage (128 bytes of each of
-// the tile's rows) goes to one of two LDS buffers; a wave reads its operands
-// half a stage (64 bytes) ahead of the instructions that use them:
+// B x B results a workgroup (rows of x, rows of w), WM x WN waves of 32 MF x
+// 32 NF each, on 32 x 32 instructions.  A stage of an operand, 128 bytes of
+// each of the tile's B rows, is an item; items lie in a ring of 2 L + 1 slots
+// of LDS, x's of stage s at place 2 s, w's at 2 s + 1.  A wave reads its
+// operands half a stage (64 bytes) ahead of the instructions that use them:
 //
-//   read half 1 of stage t | instructions on half 0 | wait for stage t + 1, barrier
-//   start loading stage t + 2 | read half 0 of stage t + 1 | instructions on half 1
+//   A(s):  start loading x of stage s + L | read half 1 of stage s | instructions on half 0
+//          wait for stage s + 1, barrier
+//   B(s):  start loading w of stage s + L | read half 0 of stage s + 1 | instructions on half 1
 //
 // so every LDS read has half a stage of matrix instructions to arrive, every
-// load a whole stage, and one barrier a stage both ends the reads of a buffer
-// and publishes the next one.
+// load L - 1/2 stages or more, and one barrier a stage both ends the reads of
+// a stage and publishes the next.  The slot that A(s) fills is that of w of
+// stage s - 1, B(s)'s that of x of stage s, both read to the end before the
+// barrier ahead.  Loads are spread over both halves because a CU takes them
+// at 64 bytes a cycle: a stage's, started together, held the waves that
+// issued them back from their matrix instructions.
 //
 // LDS banks: a cycle serves 16 lanes of a 16-byte read from 64 banks (two
 // 128-byte rows).  Chunk c of a row is stored at c ^ f(row), f giving the 8
@@ -407,24 +426,40 @@ __device__ __forceinline__ void tile_of(const LinearParams& p, int& tm, int& tn,
 
 // The results' way through LDS (the end of the kernel): floats between the
 // rows of a wave's area (the vectors of 16 lanes in different banks), groups of
-// 32 rows it holds, and the bytes a workgroup needs for that or the stages.
+// 32 rows it holds, and the bytes a workgroup needs for that or the ring.
 template <int NF> constexpr int row_stride() { return 32 * NF + 4; }
 template <int MF> constexpr int turn_groups() { return MF < 2 ? MF : 2; }
-template <int WM, int WN, int MF, int NF>
+template <int WM, int WN, int MF, int NF, int L>
 constexpr int tile_lds() {
-    const int stages = 2 * (WM * MF + WN * NF) * 32 * kStage;
+    const int ring = (2 * L + 1) * WM * MF * 32 * kStage;
     const int turn = WM * WN * turn_groups<MF>() * 32 * row_stride<NF>() * 4;
-    return stages > turn ? stages : turn;
+    return ring > turn ? ring : turn;
 }
 
-template <int DT, int WM, int WN, int MF, int NF, bool AL>
+// The order of a half stage's instructions: the loads (LOADS) and LDS reads
+// (READS) spread evenly between the matrix instructions (MMAS).
+template <int LOADS, int READS, int MMAS>
+__device__ __forceinline__ void spread() {
+    constexpr int G = LOADS < MMAS ? LOADS : MMAS;  // groups
+    constexpr int RG = (READS + G - 1) / G, MG = MMAS / G;
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x010, (LOADS + G - 1) / G, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, RG, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, MG, 0);
+    }
+}
+
+template <int DT, int WM, int WN, int MF, int NF, int L, bool AL>
 __global__ __launch_bounds__(WM* WN * 64) void linear_tile_kernel(LinearParams p) {
     constexpr int ES = elem_size<DT>();
     constexpr int NW = WM * WN;
-    constexpr int BM = WM * MF * 32, BN = WN * NF * 32;
-    constexpr int XL = BM / 8 / NW, WL = BN / 8 / NW;  // 8-row loads of a wave
-    static_assert(XL * NW * 8 == BM && WL * NW * 8 == BN, "whole loads");
-    constexpr int BUF = (BM + BN) * kStage;
+    constexpr int B = WM * MF * 32;
+    static_assert(B == WN * NF * 32, "square tiles: every item has the same size");
+    constexpr int LPI = B / 8 / NW;  // 8-row loads of a wave an item
+    static_assert(LPI * NW * 8 == B, "whole loads");
+    constexpr int ITEM = B * kStage, RING = (2 * L + 1) * ITEM;
+    constexpr int READS = 2 * (MF + NF), MMAS = MF * NF * (DT == DT_E4M3 ? 1 : DT == DT_F32 ? 8 : DT == DT_E4M3_WIDE ? 4 : 2);
     extern __shared__ __align__(16) char lds[];
 
     const int lane = threadIdx.x & 63;
@@ -432,94 +467,78 @@ __global__ __launch_bounds__(WM* WN * 64) void linear_tile_kernel(LinearParams p
     const int wm = wave % WM, wn = wave / WM;
     int tm, tn, split;
     tile_of(p, tm, tn, split);
-    const int m0 = tm * BM, n0 = tn * BN;
+    const int m0 = tm * B, n0 = tn * B;
     const int st0 = split * p.stages_per_split;
     const int all = (p.kbytes + kStage - 1) / kStage;
     const int stages = all - st0 < p.stages_per_split ? all - st0 : p.stages_per_split;
 
-    // ---- loads: a wave's load j fills rows (wave + NW j) * 8 .. + 7 of x's
-    // (then w's) part of a buffer, lane l place l % 8 of row l / 8.  Rows past
-    // the end are the last row again (their results are not stored).
-    const char* xb = p.x + m0 * p.ldx + (long long)st0 * kStage;
-    const char* wb = p.w + n0 * p.ldw + (long long)st0 * kStage;
-    // A lane's place is the same in all its loads (its rows differ by
-    // multiples of 32), so the chunk it loads is too: byte cx (cw) of the stage.
+    // ---- loads: a wave's load j of an item fills rows (wave + NW j) * 8 .. + 7,
+    // lane l place l % 8 of row l / 8.  Rows past the end are the last row again
+    // (their results are not stored).  A lane's place is the same in all its
+    // loads (its rows differ by multiples of 32), so the chunk it loads is too:
+    // byte cx (cw) of the stage.
     static_assert(NW % 4 == 0, "rows of one lane's loads differ by multiples of 32");
+    const char* const xb = p.x + m0 * p.ldx + (long long)st0 * kStage;
+    const char* const wb = p.w + n0 * p.ldw + (long long)st0 * kStage;
     const int cx = ((lane & 7) ^ rot_x(wave * 8 + (lane >> 3))) << 4;
     const int cw = ((lane & 7) ^ rot_w(wave * 8 + (lane >> 3))) << 4;
-    unsigned xo[XL], wo[WL];
+    unsigned xo[LPI], wo[LPI];
 #pragma unroll
-    for (int j = 0; j < XL; ++j) {
+    for (int j = 0; j < LPI; ++j) {
         const int row = (wave + NW * j) * 8 + (lane >> 3);
-        xo[j] = (unsigned)((m0 + row < p.M ? row : p.M - 1 - m0) * (int)p.ldx);
+        xo[j] = (unsigned)((m0 + row < p.M ? row : p.M - 1 - m0) * (int)p.ldx) + (AL ? cx : 0);
+        wo[j] = (unsigned)((n0 + row < p.N ? row : p.N - 1 - n0) * (int)p.ldw) + (AL ? cw : 0);
     }
+    // bytes of the rows from stage st on (none past the last: those loads bring
+    // zeros that nothing reads, so that every stage waits for the same count)
+    auto left_at = [&](int st) { return st < stages ? p.kbytes - (st0 + st) * kStage : 0; };
+    // aligned rows go to LDS directly
+    auto load_item = [&](const char* base, const unsigned (&o)[LPI], int c, int st, int slot) {
+        const unsigned end = c >= left_at(st) ? kBufOut : 0;
+        char* to = lds + slot + wave * 1024;
 #pragma unroll
-    for (int j = 0; j < WL; ++j) {
-        const int row = (wave + NW * j) * 8 + (lane >> 3);
-        wo[j] = (unsigned)((n0 + row < p.N ? row : p.N - 1 - n0) * (int)p.ldw);
-    }
-    if constexpr (AL) {
+        for (int j = 0; j < LPI; ++j) load_to_lds(base + (long long)st * kStage, o[j] | end, to + j * NW * 1024);
+    };
+    // others pass through registers, two stages of them in flight
+    struct Held {
+        uint4v v[LPI];
+    };
+    Held hx[AL ? 1 : 2], hw[AL ? 1 : 2];
+    auto hold_item = [&](Held& h, const char* base, const unsigned (&o)[LPI], int c, int st) {
+        const int left = left_at(st);
+        const char* from = base + (long long)st * kStage;
+        if (left >= kStage) {
 #pragma unroll
-        for (int j = 0; j < XL; ++j) xo[j] += cx;
-#pragma unroll
-        for (int j = 0; j < WL; ++j) wo[j] += cw;
-    }
-    uint4v xr[AL ? 1 : XL], wr[AL ? 1 : WL];  // unaligned rows pass through registers
-
-    auto start_loads = [&](int st, int buf) {
-        const char* xs = xb + (long long)st * kStage;
-        const char* ws = wb + (long long)st * kStage;
-        const int left = p.kbytes - (st0 + st) * kStage;  // bytes of the rows from this stage on
-        if constexpr (AL) {
-            char* base = lds + buf * BUF + wave * 1024;
-            // past the rows' end a lane loads zeros
-            const unsigned xend = cx >= left ? kBufOut : 0, wend = cw >= left ? kBufOut : 0;
-#pragma unroll
-            for (int j = 0; j < XL; ++j)
-                load_to_lds(xs, xo[j] | xend, base + j * NW * 1024);
-#pragma unroll
-            for (int j = 0; j < WL; ++j)
-                load_to_lds(ws, wo[j] | wend, base + BM * kStage + j * NW * 1024);
+            for (int j = 0; j < LPI; ++j) __builtin_memcpy(&h.v[j], from + o[j] + c, 16);
         } else {
 #pragma unroll
-            for (int j = 0; j < XL; ++j) xr[j] = load_chunk<ES>(xs + xo[j], cx, left);
-#pragma unroll
-            for (int j = 0; j < WL; ++j) wr[j] = load_chunk<ES>(ws + wo[j], cw, left);
+            for (int j = 0; j < LPI; ++j) h.v[j] = load_chunk<ES>(from + o[j], c, left);
         }
     };
-    // the loads started last are in buffer buf once this and a barrier are passed
-    auto finish_loads = [&](int buf) {
-        if constexpr (!AL) {
-            char* base = lds + buf * BUF + wave * 1024 + lane * 16;
+    auto put_item = [&](const Held& h, int slot) {
+        char* to = lds + slot + wave * 1024 + lane * 16;
 #pragma unroll
-            for (int j = 0; j < XL; ++j) *reinterpret_cast<uint4v*>(base + j * NW * 1024) = xr[j];
-#pragma unroll
-            for (int j = 0; j < WL; ++j) *reinterpret_cast<uint4v*>(base + BM * kStage + j * NW * 1024) = wr[j];
-        }
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
+        for (int j = 0; j < LPI; ++j) *reinterpret_cast<uint4v*>(to + j * NW * 1024) = h.v[j];
     };
 
     // ---- operand reads: half s of a stage, chunks 4 s + h and 4 s + 2 + h
     const int lj = lane & 31, lh = lane >> 5;
     const int wrow = 16 * ((lj >> 2) & 1) + 4 * (lj >> 3) + (lj & 3);
     const int xa = (wm * MF * 32 + lj) * kStage + ((lh ^ rot_x(lj)) << 4);
-    const int wa = BM * kStage + (wn * NF * 32 + wrow) * kStage + ((lh ^ rot_w(wrow)) << 4);
+    const int wa = (wn * NF * 32 + wrow) * kStage + ((lh ^ rot_w(wrow)) << 4);
     struct Half {
         uint4v x[MF][2], w[NF][2];
     };
-    auto read_half = [&](Half& h, int buf, int s) {
-        const char* b = lds + buf * BUF;
+    auto read_half = [&](Half& h, int xslot, int wslot, int s) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            const int xor_ = s * 64 + c * 32;
+            const int flip = s * 64 + c * 32;
 #pragma unroll
             for (int f = 0; f < NF; ++f)
-                h.w[f][c] = *reinterpret_cast<const uint4v*>(b + (wa ^ xor_) + f * 32 * kStage);
+                h.w[f][c] = *reinterpret_cast<const uint4v*>(lds + wslot + (wa ^ flip) + f * 32 * kStage);
 #pragma unroll
             for (int f = 0; f < MF; ++f)
-                h.x[f][c] = *reinterpret_cast<const uint4v*>(b + (xa ^ xor_) + f * 32 * kStage);
+                h.x[f][c] = *reinterpret_cast<const uint4v*>(lds + xslot + (xa ^ flip) + f * 32 * kStage);
         }
     };
     floatx16 acc[MF][NF] = {};
@@ -530,25 +549,83 @@ __global__ __launch_bounds__(WM* WN * 64) void linear_tile_kernel(LinearParams p
             for (int j = 0; j < NF; ++j)
                 acc[i][j] = mma32<DT>(h.w[j][0], h.w[j][1], h.x[i][0], h.x[i][1], acc[i][j]);
     };
+    // all but the last PENDING items this wave started have arrived, everywhere
+    auto arrive = [&](auto pending) {
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(decltype(pending)::value * LPI) : "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+    auto next = [](int slot) { return slot + ITEM < RING ? slot + ITEM : 0; };
 
     Half h0, h1;
-    start_loads(0, 0);
-    finish_loads(0);
-    if (stages > 1) start_loads(1, 1);
-    read_half(h0, 0, 0);
-    for (int t = 0; t < stages - 1; ++t) {
-        const int buf = t & 1;
-        read_half(h1, buf, 1);
-        products(h0);
-        __builtin_amdgcn_sched_barrier(0);
-        finish_loads(buf ^ 1);
-        if (t + 2 < stages) start_loads(t + 2, buf);
-        __builtin_amdgcn_sched_barrier(0);
-        read_half(h0, buf ^ 1, 0);
-        products(h1);
-        __builtin_amdgcn_sched_barrier(0);
+    int xs = 0, ws = ITEM;  // the slots of stage s
+    if constexpr (AL) {
+#pragma unroll
+        for (int st = 0; st < L; ++st) {
+            load_item(xb, xo, cx, st, 2 * st * ITEM);
+            load_item(wb, wo, cw, st, (2 * st + 1) * ITEM);
+        }
+        arrive(std::integral_constant<int, 2 * L - 2>{});
+        read_half(h0, xs, ws, 0);
+        int free = 2 * L * ITEM;  // the slot to fill next: the one ahead of x's of stage s
+        for (int s = 0; s < stages - 1; ++s) {
+            __builtin_amdgcn_sched_barrier(0);
+            load_item(xb, xo, cx, s + L, free);
+            read_half(h1, xs, ws, 1);
+            products(h0);
+            spread<LPI, READS, MMAS>();
+            __builtin_amdgcn_sched_barrier(0);
+            arrive(std::integral_constant<int, 2 * L - 3>{});
+            free = xs;
+            xs = next(ws);
+            ws = next(xs);
+            load_item(wb, wo, cw, s + L, free);
+            free = next(free);
+            read_half(h0, xs, ws, 0);
+            products(h1);
+            spread<LPI, READS, MMAS>();
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        // what is left on its way is not read
+    } else {
+        // an item is loaded two stages before it is put into its slot, half a
+        // stage before the barrier that publishes it: two stages' slots at once
+        static_assert(L >= 2, "slots of the stage that is read and of the next");
+        hold_item(hx[0], xb, xo, cx, 0);
+        hold_item(hw[0], wb, wo, cw, 0);
+        hold_item(hx[1], xb, xo, cx, 1);
+        hold_item(hw[1], wb, wo, cw, 1);
+        put_item(hx[0], 0);
+        put_item(hw[0], ITEM);
+        hold_item(hx[0], xb, xo, cx, 2);
+        hold_item(hw[0], wb, wo, cw, 2);
+        arrive(std::integral_constant<int, 63 / LPI>{});
+        read_half(h0, xs, ws, 0);
+        // stage s: hx[(s + 1) % 2] holds stage s + 1
+        int px = 2 * ITEM;
+        auto stage = [&](int s, Held& x1, Held& w1) {
+            put_item(x1, px);
+            px = next(px);
+            put_item(w1, px);
+            px = next(px);
+            hold_item(x1, xb, xo, cx, s + 3);
+            read_half(h1, xs, ws, 1);
+            products(h0);
+            arrive(std::integral_constant<int, 63 / LPI>{});
+            xs = next(ws);
+            ws = next(xs);
+            hold_item(w1, wb, wo, cw, s + 3);
+            read_half(h0, xs, ws, 0);
+            products(h1);
+        };
+        int s = 0;
+        for (; s + 1 < stages - 1; s += 2) {
+            stage(s, hx[1], hw[1]);
+            stage(s + 1, hx[0], hw[0]);
+        }
+        if (s < stages - 1) stage(s, hx[1], hw[1]);
     }
-    read_half(h1, (stages - 1) & 1, 1);
+    read_half(h1, xs, ws, 1);
     products(h0);
     products(h1);
 
@@ -557,20 +634,19 @@ __global__ __launch_bounds__(WM* WN * 64) void linear_tile_kernel(LinearParams p
     // through LDS of its own, so that lanes hold 8 neighbours of a row and a
     // row's lanes are neighbours too: whole 128-byte lines of y, gate and
     // residual with NF = 2 and two-byte elements.
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();  // the buffers are free
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();  // the ring is free
     asm volatile("" ::: "memory");
     constexpr int RS = row_stride<NF>();
     constexpr int LPR = 32 * NF / 8;      // lanes a row
     constexpr int RPS = 64 / LPR;         // rows a step
-    constexpr int STEPS = 32 / RPS;       // steps a 32-row group
+    constexpr int STEPS = 2;               // steps whose side values are loaded ahead
     constexpr int GR = turn_groups<MF>();
-    float* area = reinterpret_cast<float*>(lds) + wave * GR * 32 * RS;
-    const int n = n0 + wn * NF * 32 + (lane % LPR) * 8;
-    float cs[8], cb[8];
-    if (p.S == 1) column_values<8>(p, n, cs, cb);
-#pragma unroll
-    for (int i0 = 0; i0 < MF; i0 += GR) {
+    float* const area = reinterpret_cast<float*>(lds) + wave * GR * 32 * RS;
+    const int lrow = lane / LPR, lcol = (lane % LPR) * 8;
+    const int mw = m0 + wm * MF * 32, nw = n0 + wn * NF * 32;  // the wave's first row and column
+    const int n = nw + lcol;
+    auto turn = [&](int i0) {
 #pragma unroll
         for (int i = 0; i < GR; ++i)
 #pragma unroll
@@ -580,24 +656,123 @@ __global__ __launch_bounds__(WM* WN * 64) void linear_tile_kernel(LinearParams p
                     *reinterpret_cast<floatx4*>(area + (i * 32 + lj) * RS + j * 32 + lh * 16 + r) =
                         floatx4{acc[i0 + i][j][r], acc[i0 + i][j][r + 1], acc[i0 + i][j][r + 2], acc[i0 + i][j][r + 3]};
         // a wave's LDS operations complete in order: no barrier
+    };
+    auto turned = [&](int row, float (&v)[8]) {  // row: of the area, of which lanes read RPS from here
+        __builtin_memcpy(v, __builtin_assume_aligned(area + (row + lrow) * RS + lcol, 16), 32);
+    };
+    // A tile inside y, of two-byte elements: 16 bytes a lane of y, gate and
+    // residual, whose rows a step are RPS, at a uniform address and a 32-bit
+    // offset of the lane; gate, residual and row scales of the next STEPS steps
+    // are on their way while these are finished.  Instructions are few and
+    // straight, one copy for each activation and type, because a workgroup runs
+    // them cold: on a 4096 x 8192 x 4096 product with a check per element and a
+    // choice of activation per step they took 10 us a tile of 256 x 256, a
+    // sixth of the whole.
+    auto inside = [&](auto act, auto type) {
+        constexpr int ACT = decltype(act)::value, ODT = decltype(type)::value;
+        constexpr int GROUP = RPS * STEPS;  // rows
+        const unsigned yo = (unsigned)lrow * (unsigned)p.ldy + lcol * 2;
+        const unsigned go = (unsigned)lrow * (unsigned)p.ldg + lcol * 2;
+        const unsigned ro = (unsigned)lrow * (unsigned)p.ldr + lcol * 2;
+        char* const yw = p.y + mw * p.ldy + nw * 2LL;
+        const char* const gw = p.gate ? p.gate + mw * p.ldg + nw * 2LL : nullptr;
+        const char* const rw = p.res ? p.res + mw * p.ldr + nw * 2LL : nullptr;
+        float cs[8], cb[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) cs[i] = 1.0f, cb[i] = 0.0f;
+        if (DT == DT_E4M3) __builtin_memcpy(cs, p.ws + n, 32);
+        if (p.bias) __builtin_memcpy(cb, p.bias + n, 32);
+        struct Ahead {
+            uint4v g[STEPS], r[STEPS];
+            float xs[STEPS];
+        };
+        auto fetch = [&](Ahead& a, int row0) {
+#pragma unroll
+            for (int t = 0; t < STEPS; ++t) a.g[t] = a.r[t] = uint4v{0, 0, 0, 0}, a.xs[t] = 1.0f;
+            if (gw) {
+#pragma unroll
+                for (int t = 0; t < STEPS; ++t)
+                    a.g[t] = *reinterpret_cast<const uint4v*>(gw + (row0 + t * RPS) * p.ldg + go);
+            }
+            if (rw) {
+#pragma unroll
+                for (int t = 0; t < STEPS; ++t)
+                    a.r[t] = *reinterpret_cast<const uint4v*>(rw + (row0 + t * RPS) * p.ldr + ro);
+            }
+            if (DT == DT_E4M3) {
+#pragma unroll
+                for (int t = 0; t < STEPS; ++t) a.xs[t] = p.xs[mw + row0 + t * RPS + lrow];
+            }
+        };
+        auto halves = [&](uint4v u, float (&f)[8]) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint16_t h = (uint16_t)(u[i / 2] >> (16 * (i & 1)));
+                f[i] = ODT == DT_BF16 ? Elem<DT_BF16>::to_f32(h) : (float)__builtin_bit_cast(_Float16, h);
+            }
+        };
+        Ahead now;
+        fetch(now, 0);
+#pragma unroll
+        for (int i0 = 0; i0 < MF; i0 += GR) {
+            turn(i0);
 #pragma unroll 1
-        for (int i = 0; i < GR; ++i) {
-            const int row = i * 32 + lane / LPR;
-            const int m = m0 + (wm * MF + i0) * 32 + row;
+            for (int row0 = 0; row0 < GR * 32; row0 += GROUP) {
+                Ahead then;
+                fetch(then, i0 * 32 + row0 + GROUP < MF * 32 ? i0 * 32 + row0 + GROUP : 0);  // at the end: again the first
+#pragma unroll
+                for (int t = 0; t < STEPS; ++t) {
+                    float v[8], f[8];
+                    turned(row0 + t * RPS, v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        v[i] = activated<ACT>(DT == DT_E4M3 ? fmaf(v[i] * now.xs[t], cs[i], cb[i]) : v[i] + cb[i]);
+                    if (gw) {
+                        halves(now.g[t], f);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] *= f[i];
+                    }
+                    if (rw) {
+                        halves(now.r[t], f);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] += f[i];
+                    }
+                    store_out_vec<8>(yw + (i0 * 32 + row0 + t * RPS) * p.ldy + yo, ODT, v);
+                }
+                now = then;
+            }
+        }
+    };
+    if (p.S == 1 && p.vec == 2 && m0 + B <= p.M && n0 + B <= p.N) {
+        // fp32 operands with two-byte results are left to the general form
+        if constexpr (DT == DT_BF16 || DT == DT_E4M3)
+            if (p.out_dt == DT_BF16)
+                return with_activation(p.act, [&](auto act) { inside(act, std::integral_constant<int, DT_BF16>{}); });
+        if constexpr (DT == DT_F16 || DT == DT_E4M3)
+            if (p.out_dt == DT_F16)
+                return with_activation(p.act, [&](auto act) { inside(act, std::integral_constant<int, DT_F16>{}); });
+    }
+    float cs[8], cb[8];
+    if (p.S == 1) column_values<8>(p, n, cs, cb);
+#pragma unroll
+    for (int i0 = 0; i0 < MF; i0 += GR) {
+        turn(i0);
+#pragma unroll 1
+        for (int row = 0; row < GR * 32; row += RPS * STEPS) {
+            const int m = mw + i0 * 32 + row + lrow;
             Side<8> side[STEPS];
 #pragma unroll
             for (int t = 0; t < STEPS; ++t) side[t].load(p, m + t * RPS, n);
 #pragma unroll
             for (int t = 0; t < STEPS; ++t) {
                 float v[8];
-                __builtin_memcpy(v, __builtin_assume_aligned(area + (row + t * RPS) * RS + (lane % LPR) * 8, 16), 32);
+                turned(row + t * RPS, v);
                 if (p.S > 1)
                     store_part<8>(p, split, m + t * RPS, n, v);
                 else
                     finish<8>(p, m + t * RPS, n, v, cs, cb, side[t]);
             }
         }
-        asm volatile("" ::: "memory");
     }
 }
 
@@ -629,17 +804,17 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearParams p) {
     finish<4>(p, m, n, v, s, b, side);
 }
 
-template <int DT, int WM, int WN, int MF, int NF, bool AL>
+template <int DT, int WM, int WN, int MF, int NF, int L, bool AL>
 hipError_t launch_tile(LinearParams p, int S, hipStream_t stream) {
-    constexpr int BM = WM * MF * 32, BN = WN * NF * 32;
-    constexpr int LDS = tile_lds<WM, WN, MF, NF>();
+    constexpr int B = WM * MF * 32;
+    constexpr int LDS = tile_lds<WM, WN, MF, NF, L>();
     static_assert(LDS <= 160 * 1024, "one workgroup a CU at least");
-    p.tiles_m = (p.M + BM - 1) / BM;
-    p.tiles_n = (p.N + BN - 1) / BN;
+    p.tiles_m = (p.M + B - 1) / B;
+    p.tiles_n = (p.N + B - 1) / B;
     const int stages = (p.kbytes + kStage - 1) / kStage;
     p.S = S;
     p.stages_per_split = (stages + S - 1) / S;
-    auto* kernel = linear_tile_kernel<DT, WM, WN, MF, NF, AL>;
+    auto* kernel = linear_tile_kernel<DT, WM, WN, MF, NF, L, AL>;
     static std::atomic<unsigned long long> lds_set{0};  // a bit per device
     int dev = 0;
     hipError_t e = hipGetDevice(&dev);
@@ -671,14 +846,14 @@ hipError_t launch_dt(const LinearPlan& plan, const LinearParams& p, bool aligned
         case LIN_ROW16: linear_rows_kernel<ROW_DT, 1><<<rows_grid, rows_block, 0, stream>>>(p); return hipGetLastError();
         case LIN_ROW32: linear_rows_kernel<ROW_DT, 2><<<rows_grid, rows_block, 0, stream>>>(p); return hipGetLastError();
         case LIN_T64:
-            return aligned ? launch_tile<DT, 2, 2, 1, 1, true>(p, plan.S, stream)
-                           : launch_tile<DT, 2, 2, 1, 1, false>(p, plan.S, stream);
+            return aligned ? launch_tile<DT, 2, 2, 1, 1, 4, true>(p, plan.S, stream)
+                           : launch_tile<DT, 2, 2, 1, 1, 2, false>(p, plan.S, stream);
         case LIN_T256:
-            if (aligned) return launch_tile<DT, 2, 4, 4, 2, true>(p, plan.S, stream);
-            return launch_tile<DT, 2, 2, 2, 2, false>(p, plan.S, stream);
+            if (aligned) return launch_tile<DT, 2, 4, 4, 2, 2, true>(p, plan.S, stream);
+            return launch_tile<DT, 2, 2, 2, 2, 2, false>(p, plan.S, stream);
         default:
-            return aligned ? launch_tile<DT, 2, 2, 2, 2, true>(p, plan.S, stream)
-                           : launch_tile<DT, 2, 2, 2, 2, false>(p, plan.S, stream);
+            return aligned ? launch_tile<DT, 2, 2, 2, 2, 2, true>(p, plan.S, stream)
+                           : launch_tile<DT, 2, 2, 2, 2, 2, false>(p, plan.S, stream);
     }
 }
 
