@@ -671,10 +671,10 @@ def _side() -> _TorchSide:
     return _torch_side
 
 
-def _refuse_matrix(name: str, t, device, dtype, M, D):
+def _refuse_matrix(name: str, t, index: int, dtype, M, D):
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions")
-    if not t.is_cuda or t.device != device:
+    if index < 0 or t.get_device() != index:
         raise ValueError(f"{name} must be a GPU tensor on the device of the others")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
@@ -685,21 +685,21 @@ def _refuse_matrix(name: str, t, device, dtype, M, D):
     raise ValueError(f"{name}: rows must not overlap")
 
 
-def _matrix(name: str, t, device, dtype, M: int, D: int) -> int:
+def _matrix(name: str, t, index: int, dtype, M: int, D: int) -> int:
     """Check a matrix argument; the distance between its rows, in elements."""
-    if t.shape == (M, D) and t.dtype is dtype and t.device == device:
+    if t.get_device() == index and t.dtype is dtype and t.shape == (M, D):
         ld, step = t.stride()
         if step == 1 or D <= 1:
             if M <= 1:
                 return D  # a single row has no stride to speak of
             if ld >= D:
                 return ld
-    return _refuse_matrix(name, t, device, dtype, M, D)
+    return _refuse_matrix(name, t, index, dtype, M, D)
 
 
-def _vector(name: str, t, device, n: int) -> int:
+def _vector(name: str, t, index: int, n: int) -> int:
     """Check an fp32 vector argument; its address."""
-    if t.device != device:
+    if t.get_device() != index:
         raise ValueError(f"{name} must be a GPU tensor on the device of the others")
     if t.dtype is not _side().f32 or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be {n} contiguous fp32 values")
@@ -707,11 +707,13 @@ def _vector(name: str, t, device, n: int) -> int:
 
 
 def _rows_of(name: str, t):
-    if t.dim() != 2:
+    """(device index, rows, columns) of a call's first matrix."""
+    index, shape = t.get_device(), t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must have two dimensions")
-    if not t.is_cuda:
+    if index < 0:
         raise ValueError(f"{name} must be a GPU tensor")
-    return t.shape
+    return index, shape[0], shape[1]
 
 
 def _code(dtype) -> int:
@@ -743,29 +745,29 @@ def rmsnorm(x, gain=None, residual=None, eps: float = 1e-6, out_dtype=None, h=Tr
     tensor to write, x and residual among them).  x, residual, h and out are
     [M, D] with contiguous rows; gain is fp32 [D]."""
     T = _side()
-    M, D = _rows_of("x", x)
+    index, M, D = _rows_of("x", x)
     device = x.device
-    if stream is not None or device.index != T.current_device():
+    if stream is not None or index != T.current_device():
         with _elsewhere(device, stream):
             return rmsnorm(x, gain, residual, eps, out_dtype, h, out, scale)
     xt = x.dtype
     dtype = _code(xt)
-    ldx = _matrix("x", x, device, xt, M, D)
+    ldx = _matrix("x", x, index, xt, M, D)
     gp = rp = hp = sp = None
     ldr = ldh = 0
     if gain is not None:
-        gp = _vector("gain", gain, device, D)
+        gp = _vector("gain", gain, index, D)
     if out_dtype is None:
         out_dtype = xt if out is None else out.dtype
     q8 = out_dtype is T.e4m3
     code = CT_E4M3 if q8 else _code(out_dtype)
     if residual is not None:
-        ldr = _matrix("residual", residual, device, xt, M, D)
+        ldr = _matrix("residual", residual, index, xt, M, D)
         rp = residual.data_ptr()
         if h is True:
             h, ldh = T.empty((M, D), (D, 1), dtype=xt, device=device), D
         elif h is not False and h is not None:
-            ldh = _matrix("h", h, device, xt, M, D)
+            ldh = _matrix("h", h, index, xt, M, D)
         else:
             h = None
         hp = None if h is None else h.data_ptr()
@@ -776,17 +778,17 @@ def rmsnorm(x, gain=None, residual=None, eps: float = 1e-6, out_dtype=None, h=Tr
     if out is None:
         out, ldy = T.empty((M, D), (D, 1), dtype=out_dtype, device=device), D
     else:
-        ldy = _matrix("out", out, device, out_dtype, M, D)
+        ldy = _matrix("out", out, index, out_dtype, M, D)
     if q8:
         if scale is None:
             scale = T.empty((M,), (1,), dtype=T.f32, device=device)
             sp = scale.data_ptr()
         else:
-            sp = _vector("scale", scale, device, M)
+            sp = _vector("scale", scale, index, M)
     elif scale is not None:
         raise ValueError("scale belongs to 8-bit output")
     st = _load().ct_rmsnorm_fwd(x.data_ptr(), ldx, rp, ldr, gp, hp, ldh, out.data_ptr(), ldy, sp, M, D, dtype, code,
-                                eps, T.stream(device.index))
+                                eps, T.stream(index))
     if st:
         check(st, "rmsnorm")
     return out, scale, h
@@ -796,23 +798,23 @@ def quantize_rows(x, out=None, scale=None, stream=None):
     """The rows of x [M, D] in 8 bits: (q float8_e4m3fn [M, D], scale fp32 [M]),
     x ~ scale[:, None] * q."""
     T = _side()
-    M, D = _rows_of("x", x)
+    index, M, D = _rows_of("x", x)
     device = x.device
-    if stream is not None or device.index != T.current_device():
+    if stream is not None or index != T.current_device():
         with _elsewhere(device, stream):
             return quantize_rows(x, out, scale)
     dtype = _code(x.dtype)
-    ldx = _matrix("x", x, device, x.dtype, M, D)
+    ldx = _matrix("x", x, index, x.dtype, M, D)
     if out is None:
         out, ldq = T.empty((M, D), (D, 1), dtype=T.e4m3, device=device), D
     else:
-        ldq = _matrix("out", out, device, T.e4m3, M, D)
+        ldq = _matrix("out", out, index, T.e4m3, M, D)
     if scale is None:
         scale = T.empty((M,), (1,), dtype=T.f32, device=device)
         sp = scale.data_ptr()
     else:
-        sp = _vector("scale", scale, device, M)
-    st = _load().ct_quantize_rows(x.data_ptr(), ldx, out.data_ptr(), ldq, sp, M, D, dtype, T.stream(device.index))
+        sp = _vector("scale", scale, index, M)
+    st = _load().ct_quantize_rows(x.data_ptr(), ldx, out.data_ptr(), ldq, sp, M, D, dtype, T.stream(index))
     if st:
         check(st, "quantize_rows")
     return out, scale
@@ -825,12 +827,12 @@ def _workspace_bytes(M: int, N: int, K: int, dtype: int) -> int:
 
 def _product(x, xs, w, ws, bias, act, gate, residual, out_dtype, out, stream):
     T = _side()
-    M, K = _rows_of("x", x)
+    index, M, K = _rows_of("x", x)
     device = x.device
-    if stream is not None or device.index != T.current_device():
+    if stream is not None or index != T.current_device():
         with _elsewhere(device, stream):
             return _product(x, xs, w, ws, bias, act, gate, residual, out_dtype, out, None)
-    N, K2 = _rows_of("w", w)
+    N, K2 = w.shape if w.dim() == 2 else (0, 0)
     if K != K2:
         raise ValueError(f"x has rows of {K} and w of {K2}")
     xt = x.dtype
@@ -838,10 +840,10 @@ def _product(x, xs, w, ws, bias, act, gate, residual, out_dtype, out, stream):
         dtype = _code(xt)
     else:
         dtype = CT_E4M3
-        xsp, wsp = _vector("xs", xs, device, M), _vector("ws", ws, device, N)
+        xsp, wsp = _vector("xs", xs, index, M), _vector("ws", ws, index, N)
         xt = T.e4m3
-    ldx = _matrix("x", x, device, xt, M, K)
-    ldw = _matrix("w", w, device, xt, N, K)
+    ldx = _matrix("x", x, index, xt, M, K)
+    ldw = _matrix("w", w, index, xt, N, K)
     a = ACTIVATIONS.get(act)
     if a is None:
         raise ValueError(f"unknown activation {act!r}: one of {', '.join(ACTIVATIONS)}")
@@ -853,19 +855,19 @@ def _product(x, xs, w, ws, bias, act, gate, residual, out_dtype, out, stream):
         bp = gp = rp = None
         ldg = ldr = 0
         if bias is not None:
-            bp = _vector("bias", bias, device, N)
+            bp = _vector("bias", bias, index, N)
         if gate is not None:
-            ldg = _matrix("gate", gate, device, out_dtype, M, N)
+            ldg = _matrix("gate", gate, index, out_dtype, M, N)
             gp = gate.data_ptr()
         if residual is not None:
-            ldr = _matrix("residual", residual, device, out_dtype, M, N)
+            ldr = _matrix("residual", residual, index, out_dtype, M, N)
             rp = residual.data_ptr()
         epi = ct_linear_epilogue(a, bp, gp, ldg, rp, ldr)
         ep = ctypes.addressof(epi)
     if out is None:
         out, ldy = T.empty((M, N), (N, 1), dtype=out_dtype, device=device), N
     else:
-        ldy = _matrix("out", out, device, out_dtype, M, N)
+        ldy = _matrix("out", out, index, out_dtype, M, N)
     need = _workspace_bytes(M, N, K, dtype)
     space = sp = None
     if need:
@@ -873,10 +875,10 @@ def _product(x, xs, w, ws, bias, act, gate, residual, out_dtype, out, stream):
         sp = space.data_ptr()
     if xs is None:
         st = _load().ct_linear_fwd(x.data_ptr(), ldx, w.data_ptr(), ldw, out.data_ptr(), ldy, M, N, K, dtype, code, ep,
-                                   sp, need, T.stream(device.index))
+                                   sp, need, T.stream(index))
     else:
         st = _load().ct_linear_q8_fwd(x.data_ptr(), ldx, xsp, w.data_ptr(), ldw, wsp, out.data_ptr(), ldy, M, N, K,
-                                      code, ep, sp, need, T.stream(device.index))
+                                      code, ep, sp, need, T.stream(index))
     if st:
         check(st, "linear" if xs is None else "linear_q8")
     return out

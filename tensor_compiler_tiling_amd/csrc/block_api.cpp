@@ -88,8 +88,6 @@ int check_product(int M, int N, int K, int dtype, bool q8) {
     return CT_OK;
 }
 
-long long part_bytes(const LinearPlan& plan, int M, int N) { return plan.S > 1 ? 4LL * plan.S * M * N : 0; }
-
 int linear_call(const void* x, long long ldx, const float* xs, const void* w, long long ldw, const float* ws, void* y,
                 long long ldy, int M, int N, int K, int dtype, int out_dtype, const ct_linear_epilogue* epi,
                 void* workspace, long long workspace_bytes, void* stream) {
@@ -120,7 +118,7 @@ int linear_call(const void* x, long long ldx, const float* xs, const void* w, lo
         return fail(CT_ERR_UNSUPPORTED, "rows of x and w must be at most 8 MiB apart");
     p.kbytes = K * es;
     const LinearPlan plan = linear_plan(M, N, p.kbytes, dtype);
-    const long long need = part_bytes(plan, M, N);
+    const long long need = linear_part_bytes(plan, M, N);
     if (need > 0) {
         if (!workspace || workspace_bytes < need)
             return fail(CT_ERR_INVALID_ARG, "this product needs a workspace of %lld bytes (got %lld)", need,
@@ -143,7 +141,6 @@ int linear_call(const void* x, long long ldx, const float* xs, const void* w, lo
     p.N = N;
     p.act = ep.act;
     p.out_dt = out_dtype;
-    p.S = 1;
     p.vec = aligned16(y, p.ldy) && aligned16(p.gate, p.ldg) && aligned16(p.res, p.ldr);
     const long long near = 1 << 20;
     if (p.vec && oes == 2 && p.ldy <= near && p.ldg <= near && p.ldr <= near) p.vec = 2;
@@ -189,7 +186,7 @@ long long ct_linear_workspace_bytes(int M, int N, int K, int dtype) {
     if (st != CT_OK) return st;
     if (M == 0) return 0;
     const int kbytes = K * (dtype == CT_F32 ? 4 : dtype == CT_E4M3 ? 1 : 2);
-    return ct::part_bytes(ct::linear_plan(M, N, kbytes, dtype), M, N);
+    return ct::linear_part_bytes(ct::linear_plan(M, N, kbytes, dtype), M, N);
 }
 
 }  // extern "C"

@@ -20,7 +20,7 @@ struct LinearParams {
     const char* res;     // the same
     const float* xs;     // [M], [N] row scales of 8-bit operands, or null
     const float* ws;
-    float* part;         // [S][M][N] partial sums (S > 1)
+    float* part;         // partial sums of the split tiles
     long long ldx, ldw, ldy, ldg, ldr;  // bytes
     int M, N;
     int kbytes;          // bytes of a row of x and w
@@ -28,28 +28,34 @@ struct LinearParams {
     int vec;             // 1: y, gate and residual rows are 16-byte aligned; 2: and at most 1 MiB apart,
                          // of two-byte elements
     int tiles_m, tiles_n;
-    int S, stages_per_split;
+    int full, rest;      // tiles computed whole, and the others, whose
+    int S;               // reduction is split into S parts
+    int stages_per_split;
 };
 
 // The kernel that runs a product.
 enum LinearForm {
     LIN_ROW16 = 0,  // at most 16 rows of x: weights straight to registers
     LIN_ROW32 = 1,  // at most 32
-    LIN_T64 = 2,    // 64 x 64 tiles through LDS
-    LIN_T128 = 3,   // 128 x 128
-    LIN_T256 = 4,   // 256 x 256
+    LIN_T64 = 2,    // 64 x 64 tiles through LDS, two groups of waves sharing the reduction
+    LIN_T128K = 3,  // 128 x 128, the same: a tile has a CU to itself
+    LIN_T128 = 4,   // 128 x 128, two workgroups a CU
+    LIN_T256 = 5,   // 256 x 256
 };
 
 struct LinearPlan {
     int form;
-    int S;  // parts the reduction is split into (tile forms)
+    int full;  // tiles that one workgroup computes whole (the tile forms)
+    int S;     // workgroups that share each of the others, with parts of its reduction
 };
 
 // The form and split for a product of these sizes (kbytes: bytes of a row).
 LinearPlan linear_plan(int M, int N, int kbytes, int dtype);
+// Bytes of partial sums the plan needs.
+long long linear_part_bytes(const LinearPlan& plan, int M, int N);
 // p holds everything but the tiling fields, which are filled in here.
 // aligned: rows of x and w are whole numbers of 16 bytes, 16-byte aligned.
-hipError_t launch_linear(const LinearPlan& plan, LinearParams p, int dtype, bool aligned, hipStream_t stream);
+hipError_t launch_linear(LinearPlan plan, LinearParams p, int dtype, bool aligned, hipStream_t stream);
 
 // ------------------------------------------------------------------ rows --
 // h = x + residual; y = h * rsqrt(mean h^2 + eps) * gain, or y = h where no

@@ -206,7 +206,7 @@ struct Side {
     __device__ __forceinline__ void load(const LinearParams& p, int m, int n) {
         const int oes = p.out_dt == DT_F32 ? 4 : 2;
         const bool in = m < p.M && n < p.N, vec = p.vec && n + V <= p.N;
-        xs = p.xs && in && p.S == 1 ? p.xs[m] : 1.0f;
+        xs = p.xs && in ? p.xs[m] : 1.0f;
         get(p.gate, m * p.ldg + (long long)n * oes, p, n, in, vec, 1.0f, g);
         get(p.res, m * p.ldr + (long long)n * oes, p, n, in, vec, 0.0f, r);
     }
@@ -214,7 +214,7 @@ struct Side {
                                         float none, float (&f)[V]) {
 #pragma unroll
         for (int i = 0; i < V; ++i) f[i] = none;
-        if (!base || !in || p.S > 1) return;
+        if (!base || !in) return;
         if (vec) {
             load_out_vec<V>(base + at, p.out_dt, f);
         } else {
@@ -251,20 +251,6 @@ __device__ __forceinline__ void finish(const LinearParams& p, int m, int n, cons
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (n + i < p.N) store_out(y + i * oes, p.out_dt, v[i]);
-    }
-}
-
-// Partial sums of a split reduction: [S][M][N] floats.
-template <int V>
-__device__ __forceinline__ void store_part(const LinearParams& p, int split, int m, int n, const float (&v)[V]) {
-    if (m >= p.M || n >= p.N) return;
-    float* o = p.part + ((long long)split * p.M + m) * p.N + n;
-    if (n + V <= p.N) {
-        __builtin_memcpy(o, v, V * 4);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (n + i < p.N) o[i] = v[i];
     }
 }
 
@@ -375,7 +361,8 @@ __global__ __launch_bounds__(kRowWaves * 64) void linear_rows_kernel(LinearParam
 
 // ------------------------------------------------------------- tile form --
 // B x B results a workgroup (rows of x, rows of w), WM x WN waves of 32 MF x
-// 32 NF each, on 32 x 32 instructions.  A stage of an operand, 128 bytes of
+// 32 NF each, on 32 x 32 instructions; KG such groups of waves share the
+// reduction, each with stages, slots and sums of its own, joined at the end.  A stage of an operand, 128 bytes of
 // each of the tile's B rows, is an item; items lie in a ring of 2 L + 1 slots
 // of LDS, x's of stage s at place 2 s, w's at 2 s + 1.  A wave reads its
 // operands half a stage (64 bytes) ahead of the instructions that use them:
@@ -408,15 +395,9 @@ __device__ __forceinline__ void load_to_lds(const char* base, unsigned off, char
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)to, 16, off, 0, 0, 0);
 }
 
-// The tile of workgroup b: XCD b % 8 takes one run of tiles, ordered in bands
-// of 8 row tiles, so that what runs at one time on an XCD shares its L2.
-__device__ __forceinline__ void tile_of(const LinearParams& p, int& tm, int& tn, int& split) {
-    const unsigned tiles = (unsigned)p.tiles_m * p.tiles_n, nb = tiles * p.S;
-    const unsigned xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
-    const unsigned q = nb >> 3, r = nb & 7;
-    const unsigned id = xcd * q + (xcd < r ? xcd : r) + idx;
-    split = id / tiles;
-    const unsigned t = id - split * tiles;
+// Tile t in bands of 8 row tiles, row tiles fastest: what runs at one time on
+// an XCD shares its L2.
+__device__ __forceinline__ void tile_at(const LinearParams& p, unsigned t, int& tm, int& tn) {
     const unsigned band = 8u * p.tiles_n;
     const unsigned b = t / band, in = t - b * band;
     const unsigned rows = (unsigned)p.tiles_m - b * 8 < 8 ? p.tiles_m - b * 8 : 8;
@@ -424,15 +405,27 @@ __device__ __forceinline__ void tile_of(const LinearParams& p, int& tm, int& tn,
     tm = b * 8 + (in - tn * rows);
 }
 
+// The work of this workgroup: a whole tile for the first p.full of them, a
+// part of the reduction of one of the p.rest others after that (part -1: the
+// whole).  XCD b % 8 takes one run of either.
+__device__ __forceinline__ unsigned work_of(const LinearParams& p, int& part) {
+    const bool whole = blockIdx.x < (unsigned)p.full;
+    const unsigned nb = whole ? p.full : p.rest * p.S, b = blockIdx.x - (whole ? 0 : p.full);
+    const unsigned xcd = b & 7, q = nb >> 3, r = nb & 7;
+    const unsigned id = xcd * q + (xcd < r ? xcd : r) + (b >> 3);
+    part = whole ? -1 : id / p.rest;
+    return whole ? id : p.full + (id - part * p.rest);
+}
+
 // The results' way through LDS (the end of the kernel): floats between the
 // rows of a wave's area (the vectors of 16 lanes in different banks), groups of
 // 32 rows it holds, and the bytes a workgroup needs for that or the ring.
 template <int NF> constexpr int row_stride() { return 32 * NF + 4; }
 template <int MF> constexpr int turn_groups() { return MF < 2 ? MF : 2; }
-template <int WM, int WN, int MF, int NF, int L>
+template <int WM, int WN, int MF, int NF, int KG, int L>
 constexpr int tile_lds() {
-    const int ring = (2 * L + 1) * WM * MF * 32 * kStage;
-    const int turn = WM * WN * turn_groups<MF>() * 32 * row_stride<NF>() * 4;
+    const int ring = KG * (2 * L + 1) * WM * MF * 32 * kStage;
+    const int turn = KG * WM * WN * turn_groups<MF>() * 32 * row_stride<NF>() * 4;
     return ring > turn ? ring : turn;
 }
 
@@ -450,8 +443,8 @@ __device__ __forceinline__ void spread() {
     }
 }
 
-template <int DT, int WM, int WN, int MF, int NF, int L, bool AL>
-__global__ __launch_bounds__(WM* WN * 64) void linear_tile_kernel(LinearParams p) {
+template <int DT, int WM, int WN, int MF, int NF, int KG, int L, bool AL>
+__global__ __launch_bounds__(KG* WM* WN * 64) void linear_tile_kernel(LinearParams p) {
     constexpr int ES = elem_size<DT>();
     constexpr int NW = WM * WN;
     constexpr int B = WM * MF * 32;
@@ -460,17 +453,22 @@ __global__ __launch_bounds__(WM* WN * 64) void linear_tile_kernel(LinearParams p
     static_assert(LPI * NW * 8 == B, "whole loads");
     constexpr int ITEM = B * kStage, RING = (2 * L + 1) * ITEM;
     constexpr int READS = 2 * (MF + NF), MMAS = MF * NF * (DT == DT_E4M3 ? 1 : DT == DT_F32 ? 8 : DT == DT_E4M3_WIDE ? 4 : 2);
-    extern __shared__ __align__(16) char lds[];
+    extern __shared__ __align__(16) char all_lds[];
 
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave_of_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int kg = KG > 1 ? wave_of_all / NW : 0, wave = wave_of_all - kg * NW;
+    char* const lds = all_lds + kg * RING;
     const int wm = wave % WM, wn = wave / WM;
-    int tm, tn, split;
-    tile_of(p, tm, tn, split);
+    int tm, tn, part;
+    const unsigned tile = work_of(p, part);
+    tile_at(p, tile, tm, tn);
     const int m0 = tm * B, n0 = tn * B;
-    const int st0 = split * p.stages_per_split;
+    // this workgroup's stages, of which group kg takes every KG-th
+    const int st0 = part < 0 ? 0 : part * p.stages_per_split;
     const int all = (p.kbytes + kStage - 1) / kStage;
-    const int stages = all - st0 < p.stages_per_split ? all - st0 : p.stages_per_split;
+    const int end = part < 0 || all - st0 < p.stages_per_split ? all : st0 + p.stages_per_split;
+    const int stages = (end - st0 + KG - 1) / KG;
 
     // ---- loads: a wave's load j of an item fills rows (wave + NW j) * 8 .. + 7,
     // lane l place l % 8 of row l / 8.  Rows past the end are the last row again
@@ -478,8 +476,8 @@ __global__ __launch_bounds__(WM* WN * 64) void linear_tile_kernel(LinearParams p
     // loads (its rows differ by multiples of 32), so the chunk it loads is too:
     // byte cx (cw) of the stage.
     static_assert(NW % 4 == 0, "rows of one lane's loads differ by multiples of 32");
-    const char* const xb = p.x + m0 * p.ldx + (long long)st0 * kStage;
-    const char* const wb = p.w + n0 * p.ldw + (long long)st0 * kStage;
+    const char* const xb = p.x + m0 * p.ldx + (long long)(st0 + kg) * kStage;
+    const char* const wb = p.w + n0 * p.ldw + (long long)(st0 + kg) * kStage;
     const int cx = ((lane & 7) ^ rot_x(wave * 8 + (lane >> 3))) << 4;
     const int cw = ((lane & 7) ^ rot_w(wave * 8 + (lane >> 3))) << 4;
     unsigned xo[LPI], wo[LPI];
@@ -491,13 +489,16 @@ __global__ __launch_bounds__(WM* WN * 64) void linear_tile_kernel(LinearParams p
     }
     // bytes of the rows from stage st on (none past the last: those loads bring
     // zeros that nothing reads, so that every stage waits for the same count)
-    auto left_at = [&](int st) { return st < stages ? p.kbytes - (st0 + st) * kStage : 0; };
+    auto left_at = [&](int st) {
+        const int at = st0 + kg + st * KG;
+        return at < end ? p.kbytes - at * kStage : 0;
+    };
     // aligned rows go to LDS directly
     auto load_item = [&](const char* base, const unsigned (&o)[LPI], int c, int st, int slot) {
-        const unsigned end = c >= left_at(st) ? kBufOut : 0;
+        const unsigned past = c >= left_at(st) ? kBufOut : 0;
         char* to = lds + slot + wave * 1024;
 #pragma unroll
-        for (int j = 0; j < LPI; ++j) load_to_lds(base + (long long)st * kStage, o[j] | end, to + j * NW * 1024);
+        for (int j = 0; j < LPI; ++j) load_to_lds(base + (long long)st * (KG * kStage), o[j] | past, to + j * NW * 1024);
     };
     // others pass through registers, two stages of them in flight
     struct Held {
@@ -506,7 +507,7 @@ __global__ __launch_bounds__(WM* WN * 64) void linear_tile_kernel(LinearParams p
     Held hx[AL ? 1 : 2], hw[AL ? 1 : 2];
     auto hold_item = [&](Held& h, const char* base, const unsigned (&o)[LPI], int c, int st) {
         const int left = left_at(st);
-        const char* from = base + (long long)st * kStage;
+        const char* from = base + (long long)st * (KG * kStage);
         if (left >= kStage) {
 #pragma unroll
             for (int j = 0; j < LPI; ++j) __builtin_memcpy(&h.v[j], from + o[j] + c, 16);
@@ -640,9 +641,14 @@ __global__ __launch_bounds__(WM* WN * 64) void linear_tile_kernel(LinearParams p
     constexpr int RS = row_stride<NF>();
     constexpr int LPR = 32 * NF / 8;      // lanes a row
     constexpr int RPS = 64 / LPR;         // rows a step
-    constexpr int STEPS = 2;               // steps whose side values are loaded ahead
     constexpr int GR = turn_groups<MF>();
-    float* const area = reinterpret_cast<float*>(lds) + wave * GR * 32 * RS;
+    constexpr int SHARE = GR * 32 / KG;   // rows of the area that this wave finishes: each group of waves a share
+    constexpr int STEPS = SHARE < 2 * RPS ? 1 : 2;  // steps whose side values are loaded ahead
+    const int row_first = kg * SHARE;
+    static_assert(SHARE % (RPS * STEPS) == 0, "whole steps");
+    constexpr int AREA = GR * 32 * RS;
+    static_assert(KG == 1 || GR == MF, "groups join their sums in one turn");
+    float* const area = reinterpret_cast<float*>(all_lds) + wave * AREA;
     const int lrow = lane / LPR, lcol = (lane % LPR) * 8;
     const int mw = m0 + wm * MF * 32, nw = n0 + wn * NF * 32;  // the wave's first row and column
     const int n = nw + lcol;
@@ -653,12 +659,22 @@ __global__ __launch_bounds__(WM* WN * 64) void linear_tile_kernel(LinearParams p
             for (int j = 0; j < NF; ++j)
 #pragma unroll
                 for (int r = 0; r < 16; r += 4)
-                    *reinterpret_cast<floatx4*>(area + (i * 32 + lj) * RS + j * 32 + lh * 16 + r) =
+                    *reinterpret_cast<floatx4*>(area + kg * NW * AREA + (i * 32 + lj) * RS + j * 32 + lh * 16 + r) =
                         floatx4{acc[i0 + i][j][r], acc[i0 + i][j][r + 1], acc[i0 + i][j][r + 2], acc[i0 + i][j][r + 3]};
-        // a wave's LDS operations complete in order: no barrier
+        if constexpr (KG > 1)
+            __syncthreads();
+        else
+            asm volatile("" ::: "memory");  // a wave's LDS operations complete in order: no barrier
     };
     auto turned = [&](int row, float (&v)[8]) {  // row: of the area, of which lanes read RPS from here
         __builtin_memcpy(v, __builtin_assume_aligned(area + (row + lrow) * RS + lcol, 16), 32);
+#pragma unroll
+        for (int g = 1; g < KG; ++g) {
+            float w[8];
+            __builtin_memcpy(w, __builtin_assume_aligned(area + g * NW * AREA + (row + lrow) * RS + lcol, 16), 32);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += w[i];
+        }
     };
     // A tile inside y, of two-byte elements: 16 bytes a lane of y, gate and
     // residual, whose rows a step are RPS, at a uniform address and a 32-bit
@@ -712,14 +728,15 @@ __global__ __launch_bounds__(WM* WN * 64) void linear_tile_kernel(LinearParams p
             }
         };
         Ahead now;
-        fetch(now, 0);
+        fetch(now, row_first);
 #pragma unroll
         for (int i0 = 0; i0 < MF; i0 += GR) {
             turn(i0);
 #pragma unroll 1
-            for (int row0 = 0; row0 < GR * 32; row0 += GROUP) {
+            for (int row0 = row_first; row0 < row_first + SHARE; row0 += GROUP) {
                 Ahead then;
-                fetch(then, i0 * 32 + row0 + GROUP < MF * 32 ? i0 * 32 + row0 + GROUP : 0);  // at the end: again the first
+                const int after = i0 * 32 + row0 + GROUP;
+                fetch(then, after < (KG > 1 ? row_first + SHARE : MF * 32) ? after : row_first);  // at the end: again the first
 #pragma unroll
                 for (int t = 0; t < STEPS; ++t) {
                     float v[8], f[8];
@@ -743,7 +760,7 @@ __global__ __launch_bounds__(WM* WN * 64) void linear_tile_kernel(LinearParams p
             }
         }
     };
-    if (p.S == 1 && p.vec == 2 && m0 + B <= p.M && n0 + B <= p.N) {
+    if (part < 0 && p.vec == 2 && m0 + B <= p.M && n0 + B <= p.N) {
         // fp32 operands with two-byte results are left to the general form
         if constexpr (DT == DT_BF16 || DT == DT_E4M3)
             if (p.out_dt == DT_BF16)
@@ -753,68 +770,74 @@ __global__ __launch_bounds__(WM* WN * 64) void linear_tile_kernel(LinearParams p
                 return with_activation(p.act, [&](auto act) { inside(act, std::integral_constant<int, DT_F16>{}); });
     }
     float cs[8], cb[8];
-    if (p.S == 1) column_values<8>(p, n, cs, cb);
+    if (part < 0) column_values<8>(p, n, cs, cb);
+    float* const parts = part < 0 ? nullptr : p.part + ((long long)part * p.rest + (tile - p.full)) * B * B;
 #pragma unroll
     for (int i0 = 0; i0 < MF; i0 += GR) {
         turn(i0);
 #pragma unroll 1
-        for (int row = 0; row < GR * 32; row += RPS * STEPS) {
-            const int m = mw + i0 * 32 + row + lrow;
+        for (int row = row_first; row < row_first + SHARE; row += RPS * STEPS) {
+            const int mt = (wm * MF + i0) * 32 + row + lrow;  // row of the tile
+            float v[8];
+            if (part >= 0) {
+#pragma unroll
+                for (int t = 0; t < STEPS; ++t) {
+                    turned(row + t * RPS, v);
+                    __builtin_memcpy(__builtin_assume_aligned(parts + (mt + t * RPS) * B + wn * NF * 32 + lcol, 16), v, 32);
+                }
+                continue;
+            }
             Side<8> side[STEPS];
 #pragma unroll
-            for (int t = 0; t < STEPS; ++t) side[t].load(p, m + t * RPS, n);
+            for (int t = 0; t < STEPS; ++t) side[t].load(p, m0 + mt + t * RPS, n);
 #pragma unroll
             for (int t = 0; t < STEPS; ++t) {
-                float v[8];
                 turned(row + t * RPS, v);
-                if (p.S > 1)
-                    store_part<8>(p, split, m + t * RPS, n, v);
-                else
-                    finish<8>(p, m + t * RPS, n, v, cs, cb, side[t]);
+                finish<8>(p, m0 + mt + t * RPS, n, v, cs, cb, side[t]);
             }
         }
     }
 }
 
-// Join the parts of a split reduction, part after part, and finish.
+// Join the parts of the split tiles (B x B floats each, [S][rest]), part after
+// part, and finish: 4 neighbours a thread.
+template <int B>
 __global__ __launch_bounds__(256) void linear_join_kernel(LinearParams p) {
-    const int nv = (p.N + 3) / 4;
-    const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (id >= (long long)p.M * nv) return;
-    const int m = (int)(id / nv), n = (int)(id - (long long)m * nv) * 4;
-    const float* part = p.part + (long long)m * p.N + n;
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s[4], b[4];
-    const int S = p.S;
-    p.S = 1;  // what is left is an unsplit product's epilogue
+    const unsigned id = blockIdx.x * 256 + threadIdx.x;
+    constexpr unsigned PT = B * B / 4;  // threads a tile, a multiple of the workgroup
+    const unsigned t = id / PT, in = id - t * PT;
+    int tm, tn;
+    tile_at(p, p.full + t, tm, tn);
+    const int row = in / (B / 4), col = (in - row * (B / 4)) * 4;
+    const int m = tm * B + row, n = tn * B + col;
+    if (m >= p.M || n >= p.N) return;
     Side<4> side;
     side.load(p, m, n);
-    for (int k = 0; k < S; ++k, part += (long long)p.M * p.N) {
-        if (n + 4 <= p.N) {
-            float f[4];
-            __builtin_memcpy(f, part, 16);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] += f[i];
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (n + i < p.N) v[i] += part[i];
-        }
-    }
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s[4], b[4];
     column_values<4>(p, n, s, b);
+    const float* part = p.part + (long long)t * B * B + row * B + col;
+#pragma unroll 4
+    for (int k = 0; k < p.S; ++k) {
+        float f[4];
+        __builtin_memcpy(f, __builtin_assume_aligned(part + (long long)k * p.rest * B * B, 16), 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += f[i];
+    }
     finish<4>(p, m, n, v, s, b, side);
 }
 
-template <int DT, int WM, int WN, int MF, int NF, int L, bool AL>
-hipError_t launch_tile(LinearParams p, int S, hipStream_t stream) {
+template <int DT, int WM, int WN, int MF, int NF, int KG, int L, bool AL>
+hipError_t launch_tile(LinearParams p, const LinearPlan& plan, hipStream_t stream) {
     constexpr int B = WM * MF * 32;
-    constexpr int LDS = tile_lds<WM, WN, MF, NF, L>();
+    constexpr int LDS = tile_lds<WM, WN, MF, NF, KG, L>();
     static_assert(LDS <= 160 * 1024, "one workgroup a CU at least");
     p.tiles_m = (p.M + B - 1) / B;
     p.tiles_n = (p.N + B - 1) / B;
-    const int stages = (p.kbytes + kStage - 1) / kStage;
-    p.S = S;
-    p.stages_per_split = (stages + S - 1) / S;
-    auto* kernel = linear_tile_kernel<DT, WM, WN, MF, NF, L, AL>;
+    p.full = plan.full;
+    p.rest = p.tiles_m * p.tiles_n - plan.full;
+    p.S = plan.S;
+    p.stages_per_split = ((p.kbytes + kStage - 1) / kStage + p.S - 1) / p.S;
+    auto* kernel = linear_tile_kernel<DT, WM, WN, MF, NF, KG, L, AL>;
     static std::atomic<unsigned long long> lds_set{0};  // a bit per device
     int dev = 0;
     hipError_t e = hipGetDevice(&dev);
@@ -829,11 +852,10 @@ hipError_t launch_tile(LinearParams p, int S, hipStream_t stream) {
         lds_set.fetch_or(bit, std::memory_order_relaxed);
     }
     (void)hipGetLastError();
-    kernel<<<dim3((unsigned)(p.tiles_m * p.tiles_n * p.S)), dim3(WM * WN * 64), LDS, stream>>>(p);
+    kernel<<<dim3((unsigned)(p.full + p.rest * p.S)), dim3(KG * WM * WN * 64), LDS, stream>>>(p);
     e = hipGetLastError();
-    if (e != hipSuccess || S == 1) return e;
-    const long long items = (long long)p.M * ((p.N + 3) / 4);
-    linear_join_kernel<<<dim3((unsigned)((items + 255) / 256)), dim3(256), 0, stream>>>(p);
+    if (e != hipSuccess || p.rest == 0) return e;
+    linear_join_kernel<B><<<dim3((unsigned)(p.rest * (B * B / 1024))), dim3(256), 0, stream>>>(p);
     return hipGetLastError();
 }
 
@@ -846,35 +868,93 @@ hipError_t launch_dt(const LinearPlan& plan, const LinearParams& p, bool aligned
         case LIN_ROW16: linear_rows_kernel<ROW_DT, 1><<<rows_grid, rows_block, 0, stream>>>(p); return hipGetLastError();
         case LIN_ROW32: linear_rows_kernel<ROW_DT, 2><<<rows_grid, rows_block, 0, stream>>>(p); return hipGetLastError();
         case LIN_T64:
-            return aligned ? launch_tile<DT, 2, 2, 1, 1, 4, true>(p, plan.S, stream)
-                           : launch_tile<DT, 2, 2, 1, 1, 2, false>(p, plan.S, stream);
-        case LIN_T256:
-            if (aligned) return launch_tile<DT, 2, 4, 4, 2, 2, true>(p, plan.S, stream);
-            return launch_tile<DT, 2, 2, 2, 2, 2, false>(p, plan.S, stream);
-        default:
-            return aligned ? launch_tile<DT, 2, 2, 2, 2, 2, true>(p, plan.S, stream)
-                           : launch_tile<DT, 2, 2, 2, 2, 2, false>(p, plan.S, stream);
+            return aligned ? launch_tile<DT, 2, 2, 1, 1, 2, 2, true>(p, plan, stream)
+                           : launch_tile<DT, 2, 2, 1, 1, 2, 2, false>(p, plan, stream);
+        case LIN_T128K:
+            return aligned ? launch_tile<DT, 2, 2, 2, 2, 2, 2, true>(p, plan, stream)
+                           : launch_tile<DT, 2, 2, 2, 2, 2, 2, false>(p, plan, stream);
+        case LIN_T128:
+            return aligned ? launch_tile<DT, 2, 2, 2, 2, 1, 2, true>(p, plan, stream)
+                           : launch_tile<DT, 2, 2, 2, 2, 1, 2, false>(p, plan, stream);
+        default: return launch_tile<DT, 2, 4, 4, 2, 1, 2, true>(p, plan, stream);
     }
 }
 
 }  // namespace
 
-LinearPlan linear_plan(int M, int N, int kbytes, int dtype) {
-    if (M <= 16) return {LIN_ROW16, 1};
-    if (M <= 32) return {LIN_ROW32, 1};
-    const auto tiles = [&](int b) { return (long long)((M + b - 1) / b) * ((N + b - 1) / b); };
-    if (tiles(256) >= 256) return {LIN_T256, 1};
-    if (tiles(128) >= 256) return {LIN_T128, 1};
-    const long long t = tiles(64);
-    const int stages = (kbytes + kStage - 1) / kStage;
-    int S = 1;
-    while (t * S < 256 && S < 16 && stages / (S * 2) >= 4) S *= 2;
-    // every part has stages of its own
-    const int per = (stages + S - 1) / S;
-    return {LIN_T64, (stages + per - 1) / per};
+namespace {
+
+int tile_of_form(int form) { return form == LIN_T64 ? 64 : form == LIN_T256 ? 256 : 128; }
+
+// Microseconds of a stage on a CU that runs n workgroups of a form together
+// or one after another, measured on this card with operands in the caches: the
+// small tiles are bound by what a CU takes in (16 KB a stage of a 64 x 64
+// tile, 32 KB of a 128 x 128 one, at 70 to 90 GB/s), the large one by LDS and
+// the matrix units together, fp32 by the matrix units alone.
+double stage_us(int form, bool f32, long long n) {
+    switch (form) {
+        case LIN_T64: return f32 ? 0.45 * n : n == 1 ? 0.18 : 0.15 * n;
+        case LIN_T128K: return f32 ? 1.75 * n : n == 1 ? 0.40 : 0.48 * n;
+        case LIN_T128: return f32 ? 1.75 * n : 0.46 * n;
+        default: return f32 ? 7.0 * n : 1.5 * n;
+    }
 }
 
-hipError_t launch_linear(const LinearPlan& plan, LinearParams p, int dtype, bool aligned, hipStream_t stream) {
+// What a workgroup takes beside its stages (the first loads, the results).
+double edge_us(int form) { return form == LIN_T64 ? 2.0 : form == LIN_T256 ? 7.0 : 3.0; }
+
+}  // namespace
+
+long long linear_part_bytes(const LinearPlan& plan, int M, int N) {
+    if (plan.form < LIN_T64) return 0;
+    const long long b = tile_of_form(plan.form);
+    const long long rest = (M + b - 1) / b * ((N + b - 1) / b) - plan.full;
+    return rest * plan.S * b * b * 4;
+}
+
+// Up to 32 rows of x: the row forms, which read the weights once and split no
+// sum over workgroups.  Otherwise the tile, and what of it is split, that the
+// measured rates above expect to end first.  Whole rounds of tiles (one a CU)
+// are computed whole; the rest, or all where they do not fill the device, may
+// be split over k so that every CU has a share, at the price of writing and
+// reading the parts (4 bytes a result and part, at about 4 TB/s) and of a
+// second launch (2.5 us).  Measured, whole against split: 640 x 2048 x 2048
+// fp32 72 against 49 us (tiles past the first 256 in 8 parts), 64 x 4096 x
+// 12288 bf16 71 against 28 (all in 4), 256 x 1024 x 1024 bf16 10 against 13.
+LinearPlan linear_plan(int M, int N, int kbytes, int dtype) {
+    if (M <= 16) return {LIN_ROW16, 0, 1};
+    if (M <= 32) return {LIN_ROW32, 0, 1};
+    const bool f32 = dtype == DT_F32;
+    const int stages = (kbytes + kStage - 1) / kStage;
+    constexpr int CUS = 256;
+    auto rounds = [](long long t) { return (t + CUS - 1) / CUS; };
+    LinearPlan best{LIN_T64, 0, 1};
+    double best_us = 1e300;
+    for (int form = LIN_T64; form <= LIN_T256; ++form) {
+        const long long b = tile_of_form(form);
+        const long long t = (M + b - 1) / b * ((N + b - 1) / b);
+        const double whole = stages * stage_us(form, f32, rounds(t)) + edge_us(form) * rounds(t);
+        if (whole < best_us) best_us = whole, best = {form, (int)t, 1};
+        if (form == LIN_T256) continue;  // its parts are too large to pay
+        const long long full = t / CUS * CUS, rest = t - full;
+        if (rest == 0 || full > 8 * CUS) continue;
+        for (int want = 2; want <= 16; want *= 2) {
+            // every part has stages of its own, at least 4
+            const int per = (stages + want - 1) / want, S = (stages + per - 1) / per;
+            if (per < 4 || S < 2) break;
+            const double parts = (double)rest * S * b * b * 8 / 4e6;
+            const double us = stages * (full ? stage_us(form, f32, full / CUS) : 0.0) +
+                              per * stage_us(form, f32, rounds(rest * S)) +
+                              edge_us(form) * (full / CUS + rounds(rest * S)) + parts + 2.5;
+            if (us < best_us) best_us = us, best = {form, (int)full, S};
+        }
+    }
+    return best;
+}
+
+hipError_t launch_linear(LinearPlan plan, LinearParams p, int dtype, bool aligned, hipStream_t stream) {
+    // rows that pass through registers leave none for the largest tile
+    if (!aligned && plan.form == LIN_T256) plan = {LIN_T128, ((p.M + 127) / 128) * ((p.N + 127) / 128), 1};
     switch (dtype) {
         case DT_F32: return launch_dt<DT_F32>(plan, p, aligned, stream);
         case DT_F16: return launch_dt<DT_F16>(plan, p, aligned, stream);

@@ -102,7 +102,6 @@ def _split_shape():
 def test_workspace_is_asked_for_and_checked():
     M, need = _split_shape()
     a = {**LIN, "M": M, "N": 512, "K": 8192, "ldx": 8192, "ldw": 8192, "ldy": 512}
-    assert need % (4 * M * 512) == 0
     assert ct.ct_linear_fwd(**a) == ct.CT_ERR_INVALID_ARG
     assert str(need) in ct.ct_last_error()
     assert ct.ct_linear_fwd(**{**a, "workspace": P, "workspace_bytes": need - 1}) == ct.CT_ERR_INVALID_ARG
