@@ -706,14 +706,20 @@ def _vector(name: str, t, index: int, n: int) -> int:
     return t.data_ptr()
 
 
-def _rows_of(name: str, t):
-    """(device index, rows, columns) of a call's first matrix."""
+def _first(name: str, t):
+    """Check a call's first matrix: (device index, rows, columns, row distance)."""
     index, shape = t.get_device(), t.shape
     if len(shape) != 2:
         raise ValueError(f"{name} must have two dimensions")
     if index < 0:
         raise ValueError(f"{name} must be a GPU tensor")
-    return index, shape[0], shape[1]
+    M, D = shape
+    ld, step = t.stride()
+    if M <= 1:
+        ld = D  # a single row has no stride to speak of
+    if (step != 1 and D > 1) or ld < D:
+        _refuse_matrix(name, t, index, t.dtype, M, D)
+    return index, M, D, ld
 
 
 def _code(dtype) -> int:
@@ -745,14 +751,13 @@ def rmsnorm(x, gain=None, residual=None, eps: float = 1e-6, out_dtype=None, h=Tr
     tensor to write, x and residual among them).  x, residual, h and out are
     [M, D] with contiguous rows; gain is fp32 [D]."""
     T = _side()
-    index, M, D = _rows_of("x", x)
+    index, M, D, ldx = _first("x", x)
     device = x.device
     if stream is not None or index != T.current_device():
         with _elsewhere(device, stream):
             return rmsnorm(x, gain, residual, eps, out_dtype, h, out, scale)
     xt = x.dtype
     dtype = _code(xt)
-    ldx = _matrix("x", x, index, xt, M, D)
     gp = rp = hp = sp = None
     ldr = ldh = 0
     if gain is not None:
@@ -798,13 +803,12 @@ def quantize_rows(x, out=None, scale=None, stream=None):
     """The rows of x [M, D] in 8 bits: (q float8_e4m3fn [M, D], scale fp32 [M]),
     x ~ scale[:, None] * q."""
     T = _side()
-    index, M, D = _rows_of("x", x)
+    index, M, D, ldx = _first("x", x)
     device = x.device
     if stream is not None or index != T.current_device():
         with _elsewhere(device, stream):
             return quantize_rows(x, out, scale)
     dtype = _code(x.dtype)
-    ldx = _matrix("x", x, index, x.dtype, M, D)
     if out is None:
         out, ldq = T.empty((M, D), (D, 1), dtype=T.e4m3, device=device), D
     else:
@@ -827,7 +831,7 @@ def _workspace_bytes(M: int, N: int, K: int, dtype: int) -> int:
 
 def _product(x, xs, w, ws, bias, act, gate, residual, out_dtype, out, stream):
     T = _side()
-    index, M, K = _rows_of("x", x)
+    index, M, K, ldx = _first("x", x)
     device = x.device
     if stream is not None or index != T.current_device():
         with _elsewhere(device, stream):
@@ -842,7 +846,8 @@ def _product(x, xs, w, ws, bias, act, gate, residual, out_dtype, out, stream):
         dtype = CT_E4M3
         xsp, wsp = _vector("xs", xs, index, M), _vector("ws", ws, index, N)
         xt = T.e4m3
-    ldx = _matrix("x", x, index, xt, M, K)
+    if x.dtype is not xt:
+        raise ValueError(f"x must be {xt}, got {x.dtype}")
     ldw = _matrix("w", w, index, xt, N, K)
     a = ACTIVATIONS.get(act)
     if a is None:

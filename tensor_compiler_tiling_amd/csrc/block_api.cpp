@@ -118,7 +118,7 @@ int linear_call(const void* x, long long ldx, const float* xs, const void* w, lo
         return fail(CT_ERR_UNSUPPORTED, "rows of x and w must be at most 8 MiB apart");
     p.kbytes = K * es;
     const LinearPlan plan = linear_plan(M, N, p.kbytes, dtype);
-    const long long need = linear_part_bytes(plan, M, N);
+    const long long need = linear_workspace_bytes(plan, M, N, p.kbytes);
     if (need > 0) {
         if (!workspace || workspace_bytes < need)
             return fail(CT_ERR_INVALID_ARG, "this product needs a workspace of %lld bytes (got %lld)", need,
@@ -186,7 +186,7 @@ long long ct_linear_workspace_bytes(int M, int N, int K, int dtype) {
     if (st != CT_OK) return st;
     if (M == 0) return 0;
     const int kbytes = K * (dtype == CT_F32 ? 4 : dtype == CT_E4M3 ? 1 : 2);
-    return ct::linear_part_bytes(ct::linear_plan(M, N, kbytes, dtype), M, N);
+    return ct::linear_workspace_bytes(ct::linear_plan(M, N, kbytes, dtype), M, N, kbytes);
 }
 
 }  // extern "C"

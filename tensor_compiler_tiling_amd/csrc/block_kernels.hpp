@@ -20,7 +20,7 @@ struct LinearParams {
     const char* res;     // the same
     const float* xs;     // [M], [N] row scales of 8-bit operands, or null
     const float* ws;
-    float* part;         // partial sums of the split tiles
+    float* part;         // workspace: partial sums of the split tiles
     long long ldx, ldw, ldy, ldg, ldr;  // bytes
     int M, N;
     int kbytes;          // bytes of a row of x and w
@@ -47,12 +47,13 @@ struct LinearPlan {
     int form;
     int full;  // tiles that one workgroup computes whole (the tile forms)
     int S;     // workgroups that share each of the others, with parts of its reduction
+    int pack;  // copy x and w to rows of whole stages first
 };
 
 // The form and split for a product of these sizes (kbytes: bytes of a row).
 LinearPlan linear_plan(int M, int N, int kbytes, int dtype);
-// Bytes of partial sums the plan needs.
-long long linear_part_bytes(const LinearPlan& plan, int M, int N);
+// Bytes of workspace (partial sums, or rows copied to a pitch) the plan needs.
+long long linear_workspace_bytes(const LinearPlan& plan, int M, int N, int kbytes);
 // p holds everything but the tiling fields, which are filled in here.
 // aligned: rows of x and w are whole numbers of 16 bytes, 16-byte aligned.
 hipError_t launch_linear(LinearPlan plan, LinearParams p, int dtype, bool aligned, hipStream_t stream);

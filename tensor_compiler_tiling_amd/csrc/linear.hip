@@ -296,49 +296,97 @@ __device__ __forceinline__ uint4v load_chunk(const char* row, long long k, int k
     return v;
 }
 
+// 32 bytes from `sh` bits into the dword at p.  Loads at any dword address run
+// at full rate, loads at other addresses at less than half (8 x 4096 x 4095 fp16
+// 24 us with them, 11 with these and the shifts), so rows that start inside a
+// dword are read in whole dwords, all of them holding bytes of the row.
+__device__ __forceinline__ void load_shifted(const char* p, unsigned sh, uint4v& v0, uint4v& v1) {
+    uint4v a, b;
+    unsigned c;
+    __builtin_memcpy(&a, __builtin_assume_aligned(p, 4), 16);
+    __builtin_memcpy(&b, __builtin_assume_aligned(p + 16, 4), 16);
+    __builtin_memcpy(&c, __builtin_assume_aligned(p + (sh ? 32 : 28), 4), 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v0[i] = __builtin_amdgcn_alignbit(i < 3 ? a[i + 1] : b[0], a[i], sh);
+        v1[i] = __builtin_amdgcn_alignbit(i < 3 ? b[i + 1] : c, b[i], sh);
+    }
+}
+
 // -------------------------------------------------------------- row form --
 // Few rows of x (MF groups of 16).  Bound by reading the weights once.  A
 // workgroup takes 16 rows of w; its waves share the reduction, wave v taking
 // every NW-th stage, and lanes load both operands straight to registers in
-// the order the 16 x 16 instruction takes them (chunks l / 16 and 4 + l / 16
-// of row l % 16's 128 bytes), so every load of w is used once and nothing
-// passes through LDS before the waves' sums are joined there.
+// the order the 16 x 16 instruction takes them, 32 bytes of a stage of row l %
+// 16 (chunks l / 16 and 4 + l / 16, or, AL false, the neighbours 2 (l / 16)
+// and the next), so every load of w is used once and nothing passes through
+// LDS before the waves' sums are joined there.  AL: rows start at dwords.
 constexpr int kRowWaves = 8;
 
-template <int DT, int MF>
+template <int DT, int MF, bool AL>
 __global__ __launch_bounds__(kRowWaves * 64) void linear_rows_kernel(LinearParams p) {
     constexpr int ES = elem_size<DT>();
-    constexpr int U = MF == 1 ? 4 : 2;  // stages in flight
+    constexpr int U = (AL ? 8 : 4) / MF;  // stages in flight (bf16 1 x 4096 x 4096: 7.9 us with 8, 8.8 with 4)
+    constexpr int R = MF + 1;           // rows a lane reads: w's, then x's
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n0 = blockIdx.x * 16;
     const int lr = lane & 15, lg = lane >> 4;
-    const int wr = n0 + lr < p.N ? n0 + lr : p.N - 1;
-    const char* w = p.w + wr * p.ldw;
-    const char* x[MF];
+    const char* row[R];
+    row[0] = p.w + (n0 + lr < p.N ? n0 + lr : p.N - 1) * p.ldw;
 #pragma unroll
-    for (int f = 0; f < MF; ++f) {
-        const int m = f * 16 + lr;
-        x[f] = p.x + (m < p.M ? m : p.M - 1) * p.ldx;
+    for (int f = 0; f < MF; ++f) row[1 + f] = p.x + (f * 16 + lr < p.M ? f * 16 + lr : p.M - 1) * p.ldx;
+    const char* from[R];  // the lane's place in a stage (AL false: the dword it lies in)
+    unsigned sh[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        from[r] = row[r] + lg * (AL ? 16 : 32);
+        sh[r] = AL ? 0 : ((unsigned)(uintptr_t)from[r] & 3) * 8;
+        from[r] -= sh[r] / 8;
     }
     floatx4 acc[MF] = {};
-    const int stages = (p.kbytes + kStage - 1) / kStage;
-    for (int st0 = wave; st0 < stages; st0 += kRowWaves * U) {
-        uint4v a[U][2], b[U][MF][2];
+    struct Stage {
+        uint4v v[R][2];
+    };
+    auto load = [&](Stage& g, int st) {  // a whole stage
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const long long k = (long long)(st0 + u * kRowWaves) * kStage + lg * 16;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                a[u][h] = load_chunk<ES>(w, k + h * 64, p.kbytes);
-#pragma unroll
-                for (int f = 0; f < MF; ++f) b[u][f][h] = load_chunk<ES>(x[f], k + h * 64, p.kbytes);
+        for (int r = 0; r < R; ++r) {
+            const char* at = from[r] + (long long)st * kStage;
+            if constexpr (AL) {
+                __builtin_memcpy(&g.v[r][0], __builtin_assume_aligned(at, 4), 16);
+                __builtin_memcpy(&g.v[r][1], __builtin_assume_aligned(at + 64, 4), 16);
+            } else {
+                load_shifted(at, sh[r], g.v[r][0], g.v[r][1]);
             }
         }
+    };
+    auto multiply = [&](const Stage& g) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int f = 0; f < MF; ++f) acc[f] = mma16<DT>(g.v[0][0], g.v[0][1], g.v[1 + f][0], g.v[1 + f][1], acc[f]);
+    };
+    const int whole = p.kbytes / kStage;
+    int st = wave;
+    auto batch = [&](auto count) {  // that many of the wave's stages, all loaded before the first is used
+        constexpr int C = decltype(count)::value;
+        Stage g[C];
 #pragma unroll
-            for (int f = 0; f < MF; ++f) acc[f] = mma16<DT>(a[u][0], a[u][1], b[u][f][0], b[u][f][1], acc[f]);
+        for (int u = 0; u < C; ++u) load(g[u], st + u * kRowWaves);
+#pragma unroll
+        for (int u = 0; u < C; ++u) multiply(g[u]);
+        st += C * kRowWaves;
+    };
+    while (st + (U - 1) * kRowWaves < whole) batch(std::integral_constant<int, U>{});
+    if (U > 4 && st + 3 * kRowWaves < whole) batch(std::integral_constant<int, 4>{});
+    if (U > 2 && st + kRowWaves < whole) batch(std::integral_constant<int, 2>{});
+    if (st < whole) batch(std::integral_constant<int, 1>{});
+    if (st == whole && whole * kStage < p.kbytes) {  // the rows' ends
+        Stage g;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                g.v[r][h] = load_chunk<ES>(row[r], (long long)whole * kStage + lg * (AL ? 16 : 32) + h * (AL ? 64 : 16), p.kbytes);
+        multiply(g);
     }
     // join the waves' sums: results [row of x][row of w], wave after wave
     __shared__ __align__(16) float red[kRowWaves][MF * 256];
@@ -826,6 +874,37 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearParams p) {
     finish<4>(p, m, n, v, s, b, side);
 }
 
+// The rows of x and w, one after the other, at a pitch of whole stages, zeros
+// behind their ends.  A workgroup a row.
+__global__ __launch_bounds__(256) void linear_pack_kernel(LinearParams p, char* to, int pitch) {
+    const int r = blockIdx.x;
+    const char* from = r < p.M ? p.x + r * p.ldx : p.w + (r - p.M) * p.ldw;
+    const unsigned in = (unsigned)(uintptr_t)from & 3;
+    char* row = to + (long long)r * pitch;
+    for (int k = threadIdx.x * 16; k < pitch; k += 256 * 16) {
+        uint4v v;
+        if (k + 16 <= p.kbytes) {
+            // whole dwords, all holding bytes of the row
+            unsigned d[5];
+            __builtin_memcpy(d, __builtin_assume_aligned(from + k - in, 4), 16);
+            d[4] = 0;
+            if (in) __builtin_memcpy(d + 4, __builtin_assume_aligned(from + k - in + 16, 4), 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = __builtin_amdgcn_alignbit(d[i + 1], d[i], in * 8);
+        } else {
+            v = uint4v{0, 0, 0, 0};
+            for (int i = 0; i < 16 && k + i < p.kbytes; ++i) {
+                const unsigned e = (unsigned)(uint8_t)from[k + i] << (8 * (i & 3));
+                if (i < 4) v[0] |= e;
+                else if (i < 8) v[1] |= e;
+                else if (i < 12) v[2] |= e;
+                else v[3] |= e;
+            }
+        }
+        *reinterpret_cast<uint4v*>(row + k) = v;
+    }
+}
+
 template <int DT, int WM, int WN, int MF, int NF, int KG, int L, bool AL>
 hipError_t launch_tile(LinearParams p, const LinearPlan& plan, hipStream_t stream) {
     constexpr int B = WM * MF * 32;
@@ -864,9 +943,20 @@ hipError_t launch_dt(const LinearPlan& plan, const LinearParams& p, bool aligned
     (void)hipGetLastError();
     const dim3 rows_grid((unsigned)((p.N + 15) / 16)), rows_block(kRowWaves * 64);
     constexpr int ROW_DT = DT == DT_E4M3 ? DT_E4M3_WIDE : DT;
+    const bool at_dwords = ((uintptr_t)p.x | (uintptr_t)p.w | (uintptr_t)p.ldx | (uintptr_t)p.ldw) % 4 == 0;
     switch (plan.form) {
-        case LIN_ROW16: linear_rows_kernel<ROW_DT, 1><<<rows_grid, rows_block, 0, stream>>>(p); return hipGetLastError();
-        case LIN_ROW32: linear_rows_kernel<ROW_DT, 2><<<rows_grid, rows_block, 0, stream>>>(p); return hipGetLastError();
+        case LIN_ROW16:
+            if (at_dwords)
+                linear_rows_kernel<ROW_DT, 1, true><<<rows_grid, rows_block, 0, stream>>>(p);
+            else
+                linear_rows_kernel<ROW_DT, 1, false><<<rows_grid, rows_block, 0, stream>>>(p);
+            return hipGetLastError();
+        case LIN_ROW32:
+            if (at_dwords)
+                linear_rows_kernel<ROW_DT, 2, true><<<rows_grid, rows_block, 0, stream>>>(p);
+            else
+                linear_rows_kernel<ROW_DT, 2, false><<<rows_grid, rows_block, 0, stream>>>(p);
+            return hipGetLastError();
         case LIN_T64:
             return aligned ? launch_tile<DT, 2, 2, 1, 1, 2, 2, true>(p, plan, stream)
                            : launch_tile<DT, 2, 2, 1, 1, 2, 2, false>(p, plan, stream);
@@ -905,15 +995,19 @@ double edge_us(int form) { return form == LIN_T64 ? 2.0 : form == LIN_T256 ? 7.0
 
 }  // namespace
 
-long long linear_part_bytes(const LinearPlan& plan, int M, int N) {
+static int pack_pitch(int kbytes) { return (kbytes + kStage - 1) / kStage * kStage; }
+
+long long linear_workspace_bytes(const LinearPlan& plan, int M, int N, int kbytes) {
     if (plan.form < LIN_T64) return 0;
     const long long b = tile_of_form(plan.form);
     const long long rest = (M + b - 1) / b * ((N + b - 1) / b) - plan.full;
-    return rest * plan.S * b * b * 4;
+    return rest * plan.S * b * b * 4 + (plan.pack ? ((long long)M + N) * pack_pitch(kbytes) : 0);
 }
 
-// Up to 32 rows of x: the row forms, which read the weights once and split no
-// sum over workgroups.  Otherwise the tile, and what of it is split, that the
+// Up to 16 rows of x, and up to 32 with few weights or fp32: the row forms, which
+// read the weights once and split no sum over workgroups (24 rows, bf16: 1024 x
+// 1024 4.8 us against 5.8 on tiles, 4096 x 4096 12.3 against 11.8, 16384 x 1024
+// 12.2 against 9.2; fp32 4096 x 4096 22.2 against 25.5).  Otherwise the tile, and what of it is split, that the
 // measured rates above expect to end first.  Whole rounds of tiles (one a CU)
 // are computed whole; the rest, or all where they do not fill the device, may
 // be split over k so that every CU has a share, at the price of writing and
@@ -922,19 +1016,19 @@ long long linear_part_bytes(const LinearPlan& plan, int M, int N) {
 // fp32 72 against 49 us (tiles past the first 256 in 8 parts), 64 x 4096 x
 // 12288 bf16 71 against 28 (all in 4), 256 x 1024 x 1024 bf16 10 against 13.
 LinearPlan linear_plan(int M, int N, int kbytes, int dtype) {
-    if (M <= 16) return {LIN_ROW16, 0, 1};
-    if (M <= 32) return {LIN_ROW32, 0, 1};
     const bool f32 = dtype == DT_F32;
+    if (M <= 16) return {LIN_ROW16, 0, 1, 0};
+    if (M <= 32 && (f32 || (long long)N * kbytes <= 4 << 20)) return {LIN_ROW32, 0, 1, 0};
     const int stages = (kbytes + kStage - 1) / kStage;
     constexpr int CUS = 256;
     auto rounds = [](long long t) { return (t + CUS - 1) / CUS; };
-    LinearPlan best{LIN_T64, 0, 1};
+    LinearPlan best{LIN_T64, 0, 1, 0};
     double best_us = 1e300;
     for (int form = LIN_T64; form <= LIN_T256; ++form) {
         const long long b = tile_of_form(form);
         const long long t = (M + b - 1) / b * ((N + b - 1) / b);
         const double whole = stages * stage_us(form, f32, rounds(t)) + edge_us(form) * rounds(t);
-        if (whole < best_us) best_us = whole, best = {form, (int)t, 1};
+        if (whole < best_us) best_us = whole, best = {form, (int)t, 1, 0};
         if (form == LIN_T256) continue;  // its parts are too large to pay
         const long long full = t / CUS * CUS, rest = t - full;
         if (rest == 0 || full > 8 * CUS) continue;
@@ -946,15 +1040,36 @@ LinearPlan linear_plan(int M, int N, int kbytes, int dtype) {
             const double us = stages * (full ? stage_us(form, f32, full / CUS) : 0.0) +
                               per * stage_us(form, f32, rounds(rest * S)) +
                               edge_us(form) * (full / CUS + rounds(rest * S)) + parts + 2.5;
-            if (us < best_us) best_us = us, best = {form, (int)full, S};
+            if (us < best_us) best_us = us, best = {form, (int)full, S, 0};
         }
     }
+    // Rows whose length is no multiple of 16 bytes cannot go to LDS directly.
+    // Passing through registers costs a product about 0.7 of its time more
+    // (100 x 4096 x 4095 fp16 23 us, 16 for K = 4096; 2048 x 4096 x 4095 106 and
+    // 69), the largest tile, which has no registers to spare, more than that;
+    // copying both operands to whole stages costs their bytes twice at about
+    // 4.5 TB/s and a launch (4096 x 4096 x 4095 fp16 204 us through registers,
+    // 145 copied; e4m3 133 and 72).
+    if (kbytes % 16) best.pack = 2.0 * (M + (double)N) * kbytes / 4.5e6 + 2.5 < 0.7 * best_us;
     return best;
 }
 
 hipError_t launch_linear(LinearPlan plan, LinearParams p, int dtype, bool aligned, hipStream_t stream) {
-    // rows that pass through registers leave none for the largest tile
-    if (!aligned && plan.form == LIN_T256) plan = {LIN_T128, ((p.M + 127) / 128) * ((p.N + 127) / 128), 1};
+    if (plan.pack) {
+        const int pitch = pack_pitch(p.kbytes);
+        char* const to = (char*)p.part + linear_workspace_bytes(plan, p.M, p.N, p.kbytes) - ((long long)p.M + p.N) * pitch;
+        (void)hipGetLastError();
+        linear_pack_kernel<<<dim3((unsigned)p.M + (unsigned)p.N), dim3(256), 0, stream>>>(p, to, pitch);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        p.x = to;
+        p.w = to + (long long)p.M * pitch;
+        p.ldx = p.ldw = p.kbytes = pitch;
+        aligned = true;
+    } else if (plan.form == LIN_T256 && !aligned) {
+        // passing through registers leaves too few for the largest tile
+        plan = {LIN_T128, ((p.M + 127) / 128) * ((p.N + 127) / 128), 1, 0};
+    }
     switch (dtype) {
         case DT_F32: return launch_dt<DT_F32>(plan, p, aligned, stream);
         case DT_F16: return launch_dt<DT_F16>(plan, p, aligned, stream);
