@@ -109,6 +109,66 @@ def test_whole_numbers_are_exact(mnk, dtype):
     say(f"  {M}x{N}x{K} {dtype}: exact")
 
 
+# tiles past the last whole round split over k (640 x 2048: 320 of 64 x 64), sums
+# split over every tile, operands copied to whole stages (K no multiple of 16
+# bytes), and between 17 and 32 rows few and many weights
+PLANS = [(640, 2048, 1024), (1100, 2048, 999), (300, 4096, 1500), (300, 4096, 2048), (40, 520, 8191), (1011, 1500, 515),
+         (24, 1024, 1024), (24, 4100, 2052), (600, 4096, 320), (1500, 1500, 200), (2500, 2048, 131)]
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16, E4M3], ids=str)
+@pytest.mark.parametrize("mnk", PLANS, ids=lambda t: "x".join(map(str, t)))
+def test_whole_numbers_are_exact_however_the_work_is_divided(mnk, dtype):
+    M, N, K = mnk
+    g = gen(M + N + K)
+    x, w = whole(g, M, K), whole(g, N, K)
+    bias, res = whole(g, N), whole(g, M, N)
+    ref = product64(x, w) + bias.double() + res.double()
+    if dtype == E4M3:
+        one = torch.ones(max(M, N), device=DEV)
+        outs = (F32, F16)
+        call = lambda o: ct.linear_q8(x.to(E4M3), one[:M], w.to(E4M3), one[:N], bias, residual=res.to(o), out_dtype=o)  # noqa: E731
+    else:
+        outs = (F32,) if dtype == F32 else (F32, F16)
+        call = lambda o: ct.linear(x.to(dtype), w.to(dtype), bias, residual=res.to(o), out_dtype=o)  # noqa: E731
+    for o in outs:
+        if o == F16 and float(ref.abs().max()) > 2048:
+            continue
+        y = call(o)
+        torch.cuda.synchronize()
+        assert torch.equal(y.double(), ref), (mnk, dtype, o, int((y.double() != ref).sum()))
+
+
+def test_rows_of_y_far_apart():
+    """y, gate and residual rows more than 1 MiB apart, tiles inside y."""
+    M, N, K, ld = 300, 512, 128, 600_000
+    g = gen(51)
+    x, w = whole(g, M, K).to(BF16), whole(g, N, K).to(BF16)
+    base = torch.zeros(M * ld, dtype=F16, device=DEV).view(M, ld)
+    y, gate, res = base[:, :N], base[:, N:2 * N], base[:, 2 * N:3 * N]
+    gate.copy_(whole(g, M, N))
+    res.copy_(whole(g, M, N))
+    ct.linear(x, w, gate=gate, residual=res, out=y)
+    torch.cuda.synchronize()
+    ref = product64(x, w) * gate.double() + res.double()
+    assert float(ref.abs().max()) <= 2048 and torch.equal(y.double(), ref)
+
+
+@pytest.mark.parametrize("M", [3, 70, 2100])
+def test_one_tensor_in_several_places(M):
+    g = gen(52)
+    x = whole(g, M, 96).to(F16)
+    s = product64(x, x)
+    y = ct.linear(x, x, out_dtype=F32)
+    torch.cuda.synchronize()
+    assert torch.equal(y.double(), s)
+    t = whole(g, M, M).to(F32)
+    want = s * t.double() + t.double()
+    ct.linear(x, x, gate=t, residual=t, out=t)
+    torch.cuda.synchronize()
+    assert torch.equal(t.double(), want)
+
+
 ACT64 = {
     "none": lambda z: z,
     "relu": lambda z: z.clamp(min=0),
@@ -516,6 +576,49 @@ def test_graphs_replayed_together():
         assert torch.equal(eager, want[0]), rep
         for o, w in zip(outs, want):
             assert torch.equal(o, w), rep
+
+
+_CHILD = r"""
+import sys
+sys.path.insert(0, sys.argv[1])
+import torch
+from tensor_compiler_tiling_amd import convtile as ct
+x = torch.randint(-2, 3, (300, 515), device="cuda").float()
+w = torch.randint(-2, 3, (2048, 515), device="cuda").float()
+ref = x.double() @ w.double().t().contiguous()
+torch.cuda.synchronize()
+xh, wh = x.half(), w.half()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    y = ct.linear(xh, wh, out_dtype=torch.float32)
+    z = ct.linear(xh[:4], wh, out_dtype=torch.float32)
+    q, s, h = ct.rmsnorm(xh, None, xh, out_dtype=torch.float8_e4m3fn)
+    v = ct.linear_q8(q, s, *ct.quantize_rows(wh))
+torch.cuda.synchronize()
+for rep in range(4):
+    for t in (y, z, v):
+        t.fill_(float("nan"))
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y.double(), ref) and torch.equal(z.double(), ref[:4]), rep
+    assert bool(torch.isfinite(v).all()), rep
+eager = ct.linear_q8(*ct.rmsnorm(xh, None, xh, out_dtype=torch.float8_e4m3fn)[:2], *ct.quantize_rows(wh))
+torch.cuda.synchronize()
+assert torch.equal(eager, v)
+print("RESULT ok", flush=True)
+"""
+
+
+def test_first_work_of_a_process_may_be_captured():
+    """A fresh process whose first library calls are inside stream capture."""
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _CHILD, root], capture_output=True, text=True, timeout=100)
+    assert r.returncode == 0 and "RESULT ok" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
 
 
 def test_replay_reads_new_inputs():
