@@ -141,9 +141,8 @@ int linear_call(const void* x, long long ldx, const float* xs, const void* w, lo
     p.N = N;
     p.act = ep.act;
     p.out_dt = out_dtype;
-    p.vec = aligned16(y, p.ldy) && aligned16(p.gate, p.ldg) && aligned16(p.res, p.ldr);
     const long long near = 1 << 20;
-    if (p.vec && oes == 2 && p.ldy <= near && p.ldg <= near && p.ldr <= near) p.vec = 2;
+    p.near = oes == 2 && p.ldy <= near && p.ldg <= near && p.ldr <= near;
     const bool aligned = aligned16(x, p.ldx) && aligned16(w, p.ldw) && p.kbytes % 16 == 0;
     const hipError_t e = launch_linear(plan, p, dtype, aligned, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? CT_OK : hip_fail(e, "linear launch");

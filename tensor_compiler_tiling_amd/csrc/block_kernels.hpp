@@ -25,8 +25,7 @@ struct LinearParams {
     int M, N;
     int kbytes;          // bytes of a row of x and w
     int act, out_dt;
-    int vec;             // 1: y, gate and residual rows are 16-byte aligned; 2: and at most 1 MiB apart,
-                         // of two-byte elements
+    int near;            // y, gate and residual: two-byte elements, rows at most 1 MiB apart
     int tiles_m, tiles_n;
     int full, rest;      // tiles computed whole, and the others, whose
     int S;               // reduction is split into S parts

@@ -171,15 +171,16 @@ __device__ __forceinline__ void store_out(char* p, int dt, float v) {
         *reinterpret_cast<uint16_t*>(p) = round_half(v, dt);
 }
 
-// V neighbouring elements from a column that is a multiple of V: rows are
-// 16-byte aligned, so this is too, or to all its bytes where they are fewer.
+// V neighbouring elements, at any address their type allows: one access of up
+// to 16 bytes each, whatever its alignment (1011 x 1500 x 2047 fp16, whose rows of
+// y are 8-byte aligned: 28 us with an access an element, 26 so).
 template <int V>
 __device__ __forceinline__ void load_out_vec(const char* p, int dt, float (&f)[V]) {
     if (dt == DT_F32) {
-        __builtin_memcpy(f, __builtin_assume_aligned(p, V * 4 < 16 ? V * 4 : 16), V * 4);
+        __builtin_memcpy(f, p, V * 4);
     } else {
         uint16_t u[V];
-        __builtin_memcpy(u, __builtin_assume_aligned(p, V * 2 < 16 ? V * 2 : 16), V * 2);
+        __builtin_memcpy(u, p, V * 2);
 #pragma unroll
         for (int i = 0; i < V; ++i)
             f[i] = dt == DT_BF16 ? Elem<DT_BF16>::to_f32(u[i]) : (float)__builtin_bit_cast(_Float16, u[i]);
@@ -189,12 +190,12 @@ __device__ __forceinline__ void load_out_vec(const char* p, int dt, float (&f)[V
 template <int V>
 __device__ __forceinline__ void store_out_vec(char* p, int dt, const float (&f)[V]) {
     if (dt == DT_F32) {
-        __builtin_memcpy(__builtin_assume_aligned(p, V * 4 < 16 ? V * 4 : 16), f, V * 4);
+        __builtin_memcpy(p, f, V * 4);
     } else {
         uint16_t u[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) u[i] = round_half(f[i], dt);
-        __builtin_memcpy(__builtin_assume_aligned(p, V * 2 < 16 ? V * 2 : 16), u, V * 2);
+        __builtin_memcpy(p, u, V * 2);
     }
 }
 
@@ -205,7 +206,7 @@ struct Side {
     float g[V], r[V], xs;
     __device__ __forceinline__ void load(const LinearParams& p, int m, int n) {
         const int oes = p.out_dt == DT_F32 ? 4 : 2;
-        const bool in = m < p.M && n < p.N, vec = p.vec && n + V <= p.N;
+        const bool in = m < p.M && n < p.N, vec = n + V <= p.N;
         xs = p.xs && in ? p.xs[m] : 1.0f;
         get(p.gate, m * p.ldg + (long long)n * oes, p, n, in, vec, 1.0f, g);
         get(p.res, m * p.ldr + (long long)n * oes, p, n, in, vec, 0.0f, r);
@@ -245,7 +246,7 @@ __device__ __forceinline__ void finish(const LinearParams& p, int m, int n, cons
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] += side.r[i];
     }
-    if (p.vec && n + V <= p.N) {
+    if (n + V <= p.N) {
         store_out_vec<V>(y, p.out_dt, v);
     } else {
 #pragma unroll
@@ -756,12 +757,12 @@ __global__ __launch_bounds__(KG* WM* WN * 64) void linear_tile_kernel(LinearPara
             if (gw) {
 #pragma unroll
                 for (int t = 0; t < STEPS; ++t)
-                    a.g[t] = *reinterpret_cast<const uint4v*>(gw + (row0 + t * RPS) * p.ldg + go);
+                    __builtin_memcpy(&a.g[t], gw + (row0 + t * RPS) * p.ldg + go, 16);
             }
             if (rw) {
 #pragma unroll
                 for (int t = 0; t < STEPS; ++t)
-                    a.r[t] = *reinterpret_cast<const uint4v*>(rw + (row0 + t * RPS) * p.ldr + ro);
+                    __builtin_memcpy(&a.r[t], rw + (row0 + t * RPS) * p.ldr + ro, 16);
             }
             if (DT == DT_E4M3) {
 #pragma unroll
@@ -808,7 +809,7 @@ __global__ __launch_bounds__(KG* WM* WN * 64) void linear_tile_kernel(LinearPara
             }
         }
     };
-    if (part < 0 && p.vec == 2 && m0 + B <= p.M && n0 + B <= p.N) {
+    if (part < 0 && p.near && m0 + B <= p.M && n0 + B <= p.N) {
         // fp32 operands with two-byte results are left to the general form
         if constexpr (DT == DT_BF16 || DT == DT_E4M3)
             if (p.out_dt == DT_BF16)
@@ -882,24 +883,23 @@ __global__ __launch_bounds__(256) void linear_pack_kernel(LinearParams p, char* 
     const unsigned in = (unsigned)(uintptr_t)from & 3;
     char* row = to + (long long)r * pitch;
     for (int k = threadIdx.x * 16; k < pitch; k += 256 * 16) {
-        uint4v v;
-        if (k + 16 <= p.kbytes) {
-            // whole dwords, all holding bytes of the row
-            unsigned d[5];
+        const int left = p.kbytes - k;
+        // whole dwords, all holding bytes of the row
+        unsigned d[5] = {0, 0, 0, 0, 0};
+        if (left >= 16) {
             __builtin_memcpy(d, __builtin_assume_aligned(from + k - in, 4), 16);
-            d[4] = 0;
             if (in) __builtin_memcpy(d + 4, __builtin_assume_aligned(from + k - in + 16, 4), 4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = __builtin_amdgcn_alignbit(d[i + 1], d[i], in * 8);
         } else {
-            v = uint4v{0, 0, 0, 0};
-            for (int i = 0; i < 16 && k + i < p.kbytes; ++i) {
-                const unsigned e = (unsigned)(uint8_t)from[k + i] << (8 * (i & 3));
-                if (i < 4) v[0] |= e;
-                else if (i < 8) v[1] |= e;
-                else if (i < 12) v[2] |= e;
-                else v[3] |= e;
-            }
+#pragma unroll
+            for (int i = 0; i < 5; ++i)
+                if (4 * i - (int)in < left) __builtin_memcpy(d + i, __builtin_assume_aligned(from + k - in + 4 * i, 4), 4);
+        }
+        uint4v v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = __builtin_amdgcn_alignbit(d[i + 1], d[i], in * 8);
+            const int bytes = left - 4 * i;  // of the row in this dword
+            if (bytes < 4) v[i] = bytes <= 0 ? 0 : v[i] & ((1u << (8 * bytes)) - 1);
         }
         *reinterpret_cast<uint4v*>(row + k) = v;
     }
