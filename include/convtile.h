@@ -358,8 +358,8 @@ int ct_conv2d_nchw_depthwise(const void* x, const void* w, float* y,
  * y [M][D] is of out_dtype: CT_F32, CT_F16 or CT_BF16 (scale is NULL), or
  * CT_E4M3 with scale float [M].  Sums are fp32; a row of zeros with eps = 0 is
  * NaN, as the formula says.  h and y may each be exactly x
- * or residual (same pointer, stride and type); no other overlap.
- * Errors: CT_ERR_INVALID_ARG for M < 0, D < 1, a NULL or misaligned pointer,
+ * or residual (same pointer, stride and type), not the same one; no other
+ * overlap.  Errors: CT_ERR_INVALID_ARG for M < 0, D < 1, a NULL or misaligned pointer,
  * a stride below D, an unknown dtype, h without residual, scale missing (or
  * given without CT_E4M3), or eps negative or not finite; CT_ERR_HIP on a
  * launch failure.  Asynchronous on `stream`. */
@@ -411,9 +411,10 @@ typedef struct ct_linear_epilogue {
  * time, need one each.
  * Errors: CT_ERR_INVALID_ARG for M < 0, N or K < 1, a NULL or misaligned
  * pointer, a stride below the row's length, an unknown dtype or activation,
- * or a workspace that is too small; CT_ERR_UNSUPPORTED for M, N or a row's
- * bytes above 2^30, x or w rows more than 8 MiB apart, or more than 2^31 - 1
- * tiles; CT_ERR_HIP on a launch failure.  Asynchronous on `stream`. */
+ * y equal to x or w, or a workspace that is too small; CT_ERR_UNSUPPORTED for
+ * M, N or a row's bytes above 2^30, x or w rows more than 8 MiB apart, or
+ * results that one launch cannot cover (2^23 tiles of 64 x 64 to 256 x 256,
+ * chosen by the sizes); CT_ERR_HIP on a launch failure.  Asynchronous on `stream`. */
 int ct_linear_fwd(const void* x, long long ldx, const void* w, long long ldw,
                   void* y, long long ldy, int M, int N, int K, int dtype, int out_dtype,
                   const ct_linear_epilogue* epi, void* workspace, long long workspace_bytes,

@@ -53,6 +53,7 @@ int rows_call(const void* x, long long ldx, const void* residual, long long ldr,
     if (st == CT_OK && residual) st = check_matrix("residual", residual, ldr, D, dtype);
     if (st == CT_OK && h) st = check_matrix("h", h, ldh, D, dtype);
     if (st == CT_OK && gain) st = check_floats("gain", gain);
+    if (st == CT_OK && h == y) return fail(CT_ERR_INVALID_ARG, "h and y must not be the same");
     if (st != CT_OK) return st;
     if (out_dtype == CT_E4M3) {
         st = check_floats("scale", scale);
@@ -102,6 +103,7 @@ int linear_call(const void* x, long long ldx, const float* xs, const void* w, lo
     st = check_matrix("x", x, ldx, K, dtype);
     if (st == CT_OK) st = check_matrix("w", w, ldw, K, dtype);
     if (st == CT_OK) st = check_matrix("y", y, ldy, N, out_dtype);
+    if (st == CT_OK && (y == x || y == w)) return fail(CT_ERR_INVALID_ARG, "y must not be x or w");
     if (st == CT_OK && ep.gate) st = check_matrix("gate", ep.gate, ep.ldg, N, out_dtype);
     if (st == CT_OK && ep.residual) st = check_matrix("residual", ep.residual, ep.ldr, N, out_dtype);
     if (st == CT_OK && ep.bias) st = check_floats("bias", ep.bias);
@@ -118,6 +120,8 @@ int linear_call(const void* x, long long ldx, const float* xs, const void* w, lo
         return fail(CT_ERR_UNSUPPORTED, "rows of x and w must be at most 8 MiB apart");
     p.kbytes = K * es;
     const LinearPlan plan = linear_plan(M, N, p.kbytes, dtype);
+    if (linear_workgroups(plan, M, N) >= 1LL << 23)
+        return fail(CT_ERR_UNSUPPORTED, "%lld tiles: more than one launch takes", linear_workgroups(plan, M, N));
     const long long need = linear_workspace_bytes(plan, M, N, p.kbytes);
     if (need > 0) {
         if (!workspace || workspace_bytes < need)

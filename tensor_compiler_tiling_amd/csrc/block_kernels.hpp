@@ -51,6 +51,8 @@ struct LinearPlan {
 
 // The form and split for a product of these sizes (kbytes: bytes of a row).
 LinearPlan linear_plan(int M, int N, int kbytes, int dtype);
+// Workgroups (of at most 512 threads) the plan launches for the product itself.
+long long linear_workgroups(const LinearPlan& plan, int M, int N);
 // Bytes of workspace (partial sums, or rows copied to a pitch) the plan needs.
 long long linear_workspace_bytes(const LinearPlan& plan, int M, int N, int kbytes);
 // p holds everything but the tiling fields, which are filled in here.

@@ -881,32 +881,33 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearParams p) {
 }
 
 // The rows of x and w, one after the other, at a pitch of whole stages, zeros
-// behind their ends.  A workgroup a row.
+// behind their ends.  A workgroup takes every gridDim.x-th row.
 __global__ __launch_bounds__(256) void linear_pack_kernel(LinearParams p, char* to, int pitch) {
-    const int r = blockIdx.x;
-    const char* from = r < p.M ? p.x + r * p.ldx : p.w + (r - p.M) * p.ldw;
-    const unsigned in = (unsigned)(uintptr_t)from & 3;
-    char* row = to + (long long)r * pitch;
-    for (int k = threadIdx.x * 16; k < pitch; k += 256 * 16) {
-        const int left = p.kbytes - k;
-        // whole dwords, all holding bytes of the row
-        unsigned d[5] = {0, 0, 0, 0, 0};
-        if (left >= 16) {
-            __builtin_memcpy(d, __builtin_assume_aligned(from + k - in, 4), 16);
-            if (in) __builtin_memcpy(d + 4, __builtin_assume_aligned(from + k - in + 16, 4), 4);
-        } else {
+    for (int r = blockIdx.x; r < p.M + p.N; r += gridDim.x) {
+        const char* from = r < p.M ? p.x + r * p.ldx : p.w + (r - p.M) * p.ldw;
+        const unsigned in = (unsigned)(uintptr_t)from & 3;
+        char* row = to + (long long)r * pitch;
+        for (int k = threadIdx.x * 16; k < pitch; k += 256 * 16) {
+            const int left = p.kbytes - k;
+            // whole dwords, all holding bytes of the row
+            unsigned d[5] = {0, 0, 0, 0, 0};
+            if (left >= 16) {
+                __builtin_memcpy(d, __builtin_assume_aligned(from + k - in, 4), 16);
+                if (in) __builtin_memcpy(d + 4, __builtin_assume_aligned(from + k - in + 16, 4), 4);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 5; ++i)
-                if (4 * i - (int)in < left) __builtin_memcpy(d + i, __builtin_assume_aligned(from + k - in + 4 * i, 4), 4);
-        }
-        uint4v v;
+                for (int i = 0; i < 5; ++i)
+                    if (4 * i - (int)in < left) __builtin_memcpy(d + i, __builtin_assume_aligned(from + k - in + 4 * i, 4), 4);
+            }
+            uint4v v;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = __builtin_amdgcn_alignbit(d[i + 1], d[i], in * 8);
-            const int bytes = left - 4 * i;  // of the row in this dword
-            if (bytes < 4) v[i] = bytes <= 0 ? 0 : v[i] & ((1u << (8 * bytes)) - 1);
+            for (int i = 0; i < 4; ++i) {
+                v[i] = __builtin_amdgcn_alignbit(d[i + 1], d[i], in * 8);
+                const int bytes = left - 4 * i;  // of the row in this dword
+                if (bytes < 4) v[i] = bytes <= 0 ? 0 : v[i] & ((1u << (8 * bytes)) - 1);
+            }
+            *reinterpret_cast<uint4v*>(row + k) = v;
         }
-        *reinterpret_cast<uint4v*>(row + k) = v;
     }
 }
 
@@ -943,12 +944,6 @@ hipError_t launch_tile(LinearParams p, const LinearPlan& plan, hipStream_t strea
     return hipGetLastError();
 }
 
-long long workgroups(const LinearPlan& plan, const LinearParams& p) {
-    const long long b = plan.form == LIN_T64 ? 64 : plan.form == LIN_T256 ? 256 : 128;
-    const long long t = (p.M + b - 1) / b * ((p.N + b - 1) / b);
-    return plan.full + (t - plan.full) * plan.S;
-}
-
 template <int DT>
 hipError_t launch_dt(const LinearPlan& plan, const LinearParams& p, bool aligned, hipStream_t stream) {
     (void)hipGetLastError();
@@ -973,7 +968,7 @@ hipError_t launch_dt(const LinearPlan& plan, const LinearParams& p, bool aligned
             // a workgroup with a CU to itself takes a deeper ring (1024 x 1024 x 4096
             // bf16 20.5 -> 15.7 us); two share the CU's LDS (512 x 4096 x 4096 28.9 us,
             // 31.4 with the deeper one, which leaves room for one)
-            return workgroups(plan, p) <= 256 ? launch_tile<DT, 2, 2, 1, 1, 2, 3, true>(p, plan, stream)
+            return linear_workgroups(plan, p.M, p.N) <= 256 ? launch_tile<DT, 2, 2, 1, 1, 2, 3, true>(p, plan, stream)
                                               : launch_tile<DT, 2, 2, 1, 1, 2, 2, true>(p, plan, stream);
         case LIN_T128K:
             return aligned ? launch_tile<DT, 2, 2, 2, 2, 2, 2, true>(p, plan, stream)
@@ -1011,6 +1006,12 @@ double edge_us(int form) { return form == LIN_T64 ? 2.0 : form == LIN_T256 ? 7.0
 }  // namespace
 
 static int pack_pitch(int kbytes) { return (kbytes + kStage - 1) / kStage * kStage; }
+
+long long linear_workgroups(const LinearPlan& plan, int M, int N) {
+    if (plan.form < LIN_T64) return (N + 15LL) / 16;
+    const long long b = tile_of_form(plan.form);
+    return plan.full + ((M + b - 1) / b * ((N + b - 1) / b) - plan.full) * plan.S;
+}
 
 long long linear_workspace_bytes(const LinearPlan& plan, int M, int N, int kbytes) {
     if (plan.form < LIN_T64) return 0;
@@ -1074,7 +1075,7 @@ hipError_t launch_linear(LinearPlan plan, LinearParams p, int dtype, bool aligne
         const int pitch = pack_pitch(p.kbytes);
         char* const to = (char*)p.part + linear_workspace_bytes(plan, p.M, p.N, p.kbytes) - ((long long)p.M + p.N) * pitch;
         (void)hipGetLastError();
-        linear_pack_kernel<<<dim3((unsigned)p.M + (unsigned)p.N), dim3(256), 0, stream>>>(p, to, pitch);
+        linear_pack_kernel<<<dim3((unsigned)(p.M + p.N < 1 << 20 ? p.M + p.N : 1 << 20)), dim3(256), 0, stream>>>(p, to, pitch);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         p.x = to;

@@ -317,13 +317,24 @@ hipError_t launch_dt(const RowsParams& p, int M, bool norm, hipStream_t stream) 
 
 }  // namespace
 
-hipError_t launch_rows(const RowsParams& p, int M, int dtype, bool norm, hipStream_t stream) {
+hipError_t launch_rows(const RowsParams& q, int M, int dtype, bool norm, hipStream_t stream) {
     (void)hipGetLastError();
-    switch (dtype) {
-        case DT_F32: return launch_dt<DT_F32>(p, M, norm, stream);
-        case DT_F16: return launch_dt<DT_F16>(p, M, norm, stream);
-        default: return launch_dt<DT_BF16>(p, M, norm, stream);
+    // a grid holds fewer than 2^32 threads: at most 2^21 rows of up to 1024
+    constexpr int MOST = 1 << 21;
+    RowsParams p = q;
+    for (int m = 0; m < M; m += MOST) {
+        const int rows = M - m < MOST ? M - m : MOST;
+        const hipError_t e = dtype == DT_F32   ? launch_dt<DT_F32>(p, rows, norm, stream)
+                             : dtype == DT_F16 ? launch_dt<DT_F16>(p, rows, norm, stream)
+                                               : launch_dt<DT_BF16>(p, rows, norm, stream);
+        if (e != hipSuccess || M - m <= MOST) return e;
+        p.x += MOST * p.ldx;
+        p.y += MOST * p.ldy;
+        if (p.res) p.res += MOST * p.ldres;
+        if (p.h) p.h += MOST * p.ldh;
+        if (p.scale) p.scale += MOST;
     }
+    return hipSuccess;
 }
 
 }  // namespace ct

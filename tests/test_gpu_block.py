@@ -481,6 +481,21 @@ def test_many_rows():
     check_e4m3(q, s, x.double(), 2 * U)
 
 
+def test_more_rows_than_one_grid_takes():
+    """2^32 threads are more than one launch holds; rows of one wave and of four."""
+    g = gen(61)
+    for M, D in ((70_000_003, 8), (2_100_001, 1100)):
+        few = normal(g, 64, D).to(BF16)
+        x = few[torch.arange(M, device=DEV) % 64]
+        q, s = ct.quantize_rows(x)
+        q1, s1 = ct.quantize_rows(few)
+        torch.cuda.synchronize()
+        at = torch.tensor([0, 1, 65, (1 << 21) - 1, 1 << 21, M // 2, M - 2, M - 1], device=DEV)
+        assert torch.equal(q.view(torch.uint8)[at], q1.view(torch.uint8)[at % 64])
+        assert torch.equal(s, s1[torch.arange(M, device=DEV) % 64])
+        del x, q, s
+
+
 # --------------------------------------------- together, streams, graphs --
 class Block:
     """An MLP block as a serving program runs it: norm with the residual to 8

@@ -20,11 +20,11 @@ def _built():
         build.build()
 
 
-LIN = dict(x=P, ldx=64, w=P, ldw=64, y=P, ldy=32, M=4, N=32, K=64, dtype=ct.CT_BF16, out_dtype=ct.CT_BF16, epi=None,
+LIN = dict(x=P, ldx=64, w=2 * P, ldw=64, y=3 * P, ldy=32, M=4, N=32, K=64, dtype=ct.CT_BF16, out_dtype=ct.CT_BF16, epi=None,
            workspace=None, workspace_bytes=0, stream=0)
-Q8 = dict(x=P, ldx=64, xs=P, w=P, ldw=64, ws=P, y=P, ldy=32, M=4, N=32, K=64, out_dtype=ct.CT_BF16, epi=None,
+Q8 = dict(x=P, ldx=64, xs=P, w=2 * P, ldw=64, ws=P, y=3 * P, ldy=32, M=4, N=32, K=64, out_dtype=ct.CT_BF16, epi=None,
           workspace=None, workspace_bytes=0, stream=0)
-NORM = dict(x=P, ldx=64, residual=P, ldr=64, gain=P, h=P, ldh=64, y=P, ldy=64, scale=None, M=4, D=64,
+NORM = dict(x=P, ldx=64, residual=P, ldr=64, gain=P, h=2 * P, ldh=64, y=3 * P, ldy=64, scale=None, M=4, D=64,
             dtype=ct.CT_BF16, out_dtype=ct.CT_BF16, eps=1e-6, stream=0)
 QUANT = dict(x=P, ldx=64, q=P, ldq=64, scale=P, M=4, D=64, dtype=ct.CT_BF16, stream=0)
 
@@ -46,6 +46,24 @@ def epi(**kw):
 def test_linear_refuses(bad):
     assert ct.ct_linear_fwd(**{**LIN, **bad}) == ct.CT_ERR_INVALID_ARG
     assert ct.ct_last_error()
+
+
+@pytest.mark.parametrize("same", [dict(y=P), dict(w=3 * P, y=3 * P)], ids=str)
+def test_linear_refuses_to_write_over_its_operands(same):
+    a = {**LIN, "x": P, "w": 2 * P, **same}
+    assert ct.ct_linear_fwd(**a) == ct.CT_ERR_INVALID_ARG and "y must not be" in ct.ct_last_error()
+
+
+def test_rmsnorm_refuses_one_place_for_h_and_y():
+    assert ct.ct_rmsnorm_fwd(**{**NORM, "h": P, "y": P}) == ct.CT_ERR_INVALID_ARG
+    assert "must not be the same" in ct.ct_last_error()
+
+
+def test_linear_refuses_more_tiles_than_a_launch_takes():
+    a = {**LIN, "M": 1 << 30, "x": P, "w": 2 * P, "y": 3 * P}
+    assert ct.ct_linear_fwd(**a) == ct.CT_ERR_UNSUPPORTED
+    b = {**LIN, "M": 1, "N": 1 << 28, "ldy": 1 << 28, "x": P, "w": 2 * P, "y": 3 * P}
+    assert ct.ct_linear_fwd(**b) == ct.CT_ERR_UNSUPPORTED
 
 
 @pytest.mark.parametrize("bad", [
