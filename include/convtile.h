@@ -357,7 +357,8 @@ int ct_conv2d_nchw_depthwise(const void* x, const void* w, float* y,
  * dtype) may be NULL if it is not wanted; y is made from the unrounded sum.
  * y [M][D] is of out_dtype: CT_F32, CT_F16 or CT_BF16 (scale is NULL), or
  * CT_E4M3 with scale float [M].  Sums are fp32; a row of zeros with eps = 0 is
- * NaN, as the formula says.  h and y may each be exactly x
+ * NaN, and one whose squares pass the range of fp32 zeros, as the formula says
+ * in fp32.  h and y may each be exactly x
  * or residual (same pointer, stride and type), not the same one; no other
  * overlap.  Errors: CT_ERR_INVALID_ARG for M < 0, D < 1, a NULL or misaligned pointer,
  * a stride below D, an unknown dtype, h without residual, scale missing (or
@@ -370,7 +371,7 @@ int ct_rmsnorm_fwd(const void* x, long long ldx, const void* residual, long long
 
 /* Rows x [M][D] (CT_F32, CT_F16 or CT_BF16) to e4m3 q [M][D] with scale [M],
  * as above: a layer's weights once, and activations that no norm produces.
- * Errors as for ct_rmsnorm_fwd. */
+ * q must not overlap x.  Errors as for ct_rmsnorm_fwd. */
 int ct_quantize_rows(const void* x, long long ldx, void* q, long long ldq, float* scale,
                      int M, int D, int dtype, void* stream);
 

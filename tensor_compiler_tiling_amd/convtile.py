@@ -646,6 +646,7 @@ def conv2d_depthwise(x, w, stride: int = 1, pad: int = 0, epilogue: int = CT_EPI
 
 
 # ---- transformer-block rows: matrices whose rows may lie apart -------------
+# Forward only, like everything here: results carry no autograd history.
 # The smallest calls take a few microseconds on the device, less than a careless
 # wrapper takes on the host: what these helpers need of torch is looked up once,
 # and a well-formed argument passes its checks in one comparison.

@@ -307,6 +307,18 @@ def test_nan_and_infinity_reach_their_row_alone(M, dtype):
         assert torch.equal(y.double(), product64(x, w))
 
 
+@pytest.mark.parametrize("dtype,a,b", [(F32, 2.0 ** -140, 2.0 ** 100), (F32, 2.0 ** -80, 2.0 ** -60), (F16, 2.0 ** -24, 1.0),
+                                       (BF16, 2.0 ** -130, 2.0 ** 100)], ids=str)
+@pytest.mark.parametrize("M", [1, 20, 70, 2100])
+def test_subnormal_values_count(M, dtype, a, b):
+    """Subnormal operands and results are kept: powers of two, exact in fp32."""
+    x = torch.full((M, 64), a, device=DEV).to(dtype)
+    w = torch.full((2100, 64), b, device=DEV).to(dtype)
+    y = ct.linear(x, w, out_dtype=F32)
+    torch.cuda.synchronize()
+    assert bool((y.double() == 64 * a * b).all())
+
+
 def test_garbage_past_the_rows_end_is_not_read_into_results():
     """Whatever lies between the rows (NaN here) stays out of the sums."""
     for M, N, K in ((3, 20, 40), (40, 70, 200), (70, 70, 72)):
