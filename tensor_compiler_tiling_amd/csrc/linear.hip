@@ -11,8 +11,8 @@
 // The weights are the instruction's first operand (its rows) and x the second
 // (its columns): a lane's results then belong to one row of x, and the rows
 // of w are dealt to the instruction's rows so that they are neighbours in it
-// (4, or 16 with 32 x 32 instructions): y, gate and residual are read and
-// written in 16-byte vectors straight from the accumulators' lanes.
+// (4, or 16 with 32 x 32 instructions), which go on to LDS in 16-byte vectors
+// and come back as whole lines of y, gate and residual.
 #include "ct_device.hpp"
 #include "block_kernels.hpp"
 
@@ -299,7 +299,7 @@ __device__ __forceinline__ uint4v load_chunk(const char* row, long long k, int k
 
 // 32 bytes from `sh` bits into the dword at p.  Loads at any dword address run
 // at full rate, loads at other addresses at less than half (8 x 4096 x 4095 fp16
-// 24 us with them, 11 with these and the shifts), so rows that start inside a
+// 24 us with them, 13 with these and the shifts), so rows that start inside a
 // dword are read in whole dwords, all of them holding bytes of the row.
 __device__ __forceinline__ void load_shifted(const char* p, unsigned sh, uint4v& v0, uint4v& v1) {
     uint4v a, b;
@@ -322,6 +322,8 @@ __device__ __forceinline__ void load_shifted(const char* p, unsigned sh, uint4v&
 // 16 (chunks l / 16 and 4 + l / 16, or, AL false, the neighbours 2 (l / 16)
 // and the next), so every load of w is used once and nothing passes through
 // LDS before the waves' sums are joined there.  AL: rows start at dwords.
+// Measured: one row, bf16, 8192 x 8192 weights (not in the caches) 28 us, 4.8
+// TB/s, where a device copy moves 5.1 to 5.2; 4096 x 4096 (in them) 7.9 us.
 constexpr int kRowWaves = 8;
 
 template <int DT, int MF, bool AL>
@@ -411,10 +413,11 @@ __global__ __launch_bounds__(kRowWaves * 64) void linear_rows_kernel(LinearParam
 // ------------------------------------------------------------- tile form --
 // B x B results a workgroup (rows of x, rows of w), WM x WN waves of 32 MF x
 // 32 NF each, on 32 x 32 instructions; KG such groups of waves share the
-// reduction, each with stages, slots and sums of its own, joined at the end.  A stage of an operand, 128 bytes of
-// each of the tile's B rows, is an item; items lie in a ring of 2 L + 1 slots
-// of LDS, x's of stage s at place 2 s, w's at 2 s + 1.  A wave reads its
-// operands half a stage (64 bytes) ahead of the instructions that use them:
+// reduction, each with stages, slots and sums of its own, joined at the end.
+// A stage of an operand, 128 bytes of each of the tile's B rows, is an item;
+// items lie in a ring of 2 L + 1 slots of LDS, x's of stage s at place 2 s, w's
+// at 2 s + 1.  A wave reads its operands half a stage (64 bytes) ahead of the
+// instructions that use them:
 //
 //   A(s):  start loading x of stage s + L | read half 1 of stage s | instructions on half 0
 //          wait for stage s + 1, barrier
@@ -427,6 +430,13 @@ __global__ __launch_bounds__(kRowWaves * 64) void linear_rows_kernel(LinearParam
 // barrier ahead.  Loads are spread over both halves because a CU takes them
 // at 64 bytes a cycle: a stage's, started together, held the waves that
 // issued them back from their matrix instructions.
+//
+// The 256 x 256 tile is bound by the matrix units (70% busy) and the issue of
+// loads: 4096 x 8192 x 4096 bf16 217 to 229 us with the boxes' clocks (1.2 to 1.27
+// PFLOP/s), 8192 x 8192 x 8192 bf16 814 (1.35), e4m3 416 (2.64), fp32 4096 x 4096 x
+// 4096 945 (145 TFLOP/s).  The smaller ones, taken where that would leave CUs
+// idle, are bound by what a CU takes in from L2, 75 GB/s (1024 x 1024 x 4096 bf16,
+// 64 x 64, 15.7 us; 2048 x 2048 x 2048, 128 x 128, 21 to 23).
 //
 // LDS banks: a cycle serves 16 lanes of a 16-byte read from 64 banks (two
 // 128-byte rows).  Chunk c of a row is stored at c ^ f(row), f giving the 8
@@ -516,6 +526,7 @@ __global__ __launch_bounds__(KG* WM* WN * 64) void linear_tile_kernel(LinearPara
     const int wm = wave % WM, wn = wave / WM;
     int tm, tn, part;
     const unsigned tile = work_of(p, part);
+    if (B == 256) part = -1;  // never split
     tile_at(p, tile, tm, tn);
     const int m0 = tm * B, n0 = tn * B;
     // this workgroup's stages, of which group kg takes every KG-th
@@ -939,9 +950,12 @@ hipError_t launch_tile(LinearParams p, const LinearPlan& plan, hipStream_t strea
     (void)hipGetLastError();
     kernel<<<dim3((unsigned)(p.full + p.rest * p.S)), dim3(KG * WM * WN * 64), LDS, stream>>>(p);
     e = hipGetLastError();
-    if (e != hipSuccess || p.rest == 0) return e;
-    linear_join_kernel<B><<<dim3((unsigned)(p.rest * (B * B / 1024))), dim3(256), 0, stream>>>(p);
-    return hipGetLastError();
+    if constexpr (B < 256) {  // the largest tiles are never split
+        if (e != hipSuccess || p.rest == 0) return e;
+        linear_join_kernel<B><<<dim3((unsigned)(p.rest * (B * B / 1024))), dim3(256), 0, stream>>>(p);
+        e = hipGetLastError();
+    }
+    return e;
 }
 
 template <int DT>
@@ -968,8 +982,8 @@ hipError_t launch_dt(const LinearPlan& plan, const LinearParams& p, bool aligned
             // a workgroup with a CU to itself takes a deeper ring (1024 x 1024 x 4096
             // bf16 20.5 -> 15.7 us); two share the CU's LDS (512 x 4096 x 4096 28.9 us,
             // 31.4 with the deeper one, which leaves room for one)
-            return linear_workgroups(plan, p.M, p.N) <= 256 ? launch_tile<DT, 2, 2, 1, 1, 2, 3, true>(p, plan, stream)
-                                              : launch_tile<DT, 2, 2, 1, 1, 2, 2, true>(p, plan, stream);
+            if (linear_workgroups(plan, p.M, p.N) <= 256) return launch_tile<DT, 2, 2, 1, 1, 2, 3, true>(p, plan, stream);
+            return launch_tile<DT, 2, 2, 1, 1, 2, 2, true>(p, plan, stream);
         case LIN_T128K:
             return aligned ? launch_tile<DT, 2, 2, 2, 2, 2, 2, true>(p, plan, stream)
                            : launch_tile<DT, 2, 2, 2, 2, 2, 2, false>(p, plan, stream);
