@@ -1037,14 +1037,15 @@ long long linear_workspace_bytes(const LinearPlan& plan, int M, int N, int kbyte
 // Up to 16 rows of x, and up to 32 with few weights or fp32: the row forms, which
 // read the weights once and split no sum over workgroups (24 rows, bf16: 1024 x
 // 1024 4.8 us against 5.8 on tiles, 4096 x 4096 12.3 against 11.8, 16384 x 1024
-// 12.2 against 9.2; fp32 4096 x 4096 22.2 against 25.5).  Otherwise the tile, and what of it is split, that the
-// measured rates above expect to end first.  Whole rounds of tiles (one a CU)
-// are computed whole; the rest, or all where they do not fill the device, may
-// be split over k so that every CU has a share, at the price of writing and
-// reading the parts (4 bytes a result and part, at about 4 TB/s) and of a
-// second launch (2.5 us).  Measured, whole against split: 640 x 2048 x 2048
-// fp32 72 against 49 us (tiles past the first 256 in 8 parts), 64 x 4096 x
-// 12288 bf16 71 against 28 (all in 4), 256 x 1024 x 1024 bf16 10 against 13.
+// 12.2 against 9.2; fp32 4096 x 4096 22.2 against 25.5).  Otherwise the tile, and
+// what of it is split, that the measured rates above expect to end first.
+// Whole rounds of tiles (one a CU) are computed whole; the rest, or all where
+// they do not fill the device, may be split over k so that every CU has a
+// share, at the price of writing and reading the parts (4 bytes a result and
+// part, at about 4 TB/s) and of a second launch (2.5 us; 4 after whole tiles,
+// whose CUs the parts share).  Measured, whole against split: 640 x 2048 x 2048
+// fp32 72 against 49 us (tiles past the first 256 in 4 parts), 64 x 4096 x 12288
+// bf16 71 against 28 (all in 4), 256 x 1024 x 1024 bf16 10 against 13.
 LinearPlan linear_plan(int M, int N, int kbytes, int dtype) {
     const bool f32 = dtype == DT_F32;
     if (M <= 16) return {LIN_ROW16, 0, 1, 0};
@@ -1062,25 +1063,27 @@ LinearPlan linear_plan(int M, int N, int kbytes, int dtype) {
         if (form == LIN_T256) continue;  // its parts are too large to pay
         const long long full = t / CUS * CUS, rest = t - full;
         if (rest == 0 || full > 8 * CUS) continue;
-        for (int want = 2; want <= 16; want *= 2) {
+        for (int want = 2; want <= 16; ++want) {
             // every part has stages of its own, at least 4
             const int per = (stages + want - 1) / want, S = (stages + per - 1) / per;
             if (per < 4 || S < 2) break;
             const double parts = (double)rest * S * b * b * 8 / 4e6;
             const double us = stages * (full ? stage_us(form, f32, full / CUS) : 0.0) +
                               per * stage_us(form, f32, rounds(rest * S)) +
-                              edge_us(form) * (full / CUS + rounds(rest * S)) + parts + 2.5;
+                              edge_us(form) * (full / CUS + rounds(rest * S)) + parts + (full ? 4.0 : 2.5);
             if (us < best_us) best_us = us, best = {form, (int)full, S, 0};
         }
     }
     // Rows whose length is no multiple of 16 bytes cannot go to LDS directly.
     // Passing through registers costs a product about 0.7 of its time more
     // (100 x 4096 x 4095 fp16 23 us, 16 for K = 4096; 2048 x 4096 x 4095 106 and
-    // 69), the largest tile, which has no registers to spare, more than that;
+    // 69), the largest tile, which has no registers to spare, more than that, and
+    // fp32, which the matrix units bound, a sixth (2048 x 2048 x 2047 145 us, 127;
+    // 1472 x 169 x 11597 69, 99 copied);
     // copying both operands to whole stages costs their bytes twice at about
     // 4.5 TB/s and a launch (4096 x 4096 x 4095 fp16 204 us through registers,
-    // 145 copied; e4m3 133 and 72).
-    if (kbytes % 16) best.pack = 2.0 * (M + (double)N) * kbytes / 4.5e6 + 2.5 < 0.7 * best_us;
+    // 150 copied; e4m3 133 and 74).
+    if (kbytes % 16) best.pack = 2.0 * (M + (double)N) * kbytes / 4.5e6 + 2.5 < (f32 ? 0.17 : 0.7) * best_us;
     return best;
 }
 
