@@ -16,6 +16,7 @@
 #include "ct_device.hpp"
 #include "block_kernels.hpp"
 
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 
@@ -1034,11 +1035,16 @@ long long linear_workspace_bytes(const LinearPlan& plan, int M, int N, int kbyte
     return rest * plan.S * b * b * 4 + (plan.pack ? ((long long)M + N) * pack_pitch(kbytes) : 0);
 }
 
-// Up to 16 rows of x, and up to 32 with few weights or fp32: the row forms, which
-// read the weights once and split no sum over workgroups (24 rows, bf16: 1024 x
-// 1024 4.8 us against 5.8 on tiles, 4096 x 4096 12.3 against 11.8, 16384 x 1024
-// 12.2 against 9.2; fp32 4096 x 4096 22.2 against 25.5).  Otherwise the tile, and
-// what of it is split, that the measured rates above expect to end first.
+// Microseconds of a row form: its waves' turns of 8 stages (0.7 us, 1.2 with two
+// groups of rows), or the weights' bytes, or, with two groups, the weights' and
+// twice as many of x's from L2.
+static double row_us(int M, int N, int kbytes) {
+    const double turns = (kbytes + 8 * kStage - 1) / (8 * kStage), bytes = (double)N * kbytes;
+    return M <= 16 ? std::max(2.5 + 0.7 * turns, 1.5 + bytes / 4.8e6) : std::max(2.5 + 1.2 * turns, 2.0 + 3.0 * bytes / 10e6);
+}
+
+// The tile, and what of it is split, that the measured rates above expect to
+// end first.
 // Whole rounds of tiles (one a CU) are computed whole; the rest, or all where
 // they do not fill the device, may be split over k so that every CU has a
 // share, at the price of writing and reading the parts (4 bytes a result and
@@ -1046,10 +1052,16 @@ long long linear_workspace_bytes(const LinearPlan& plan, int M, int N, int kbyte
 // whose CUs the parts share).  Measured, whole against split: 640 x 2048 x 2048
 // fp32 72 against 49 us (tiles past the first 256 in 4 parts), 64 x 4096 x 12288
 // bf16 71 against 28 (all in 4), 256 x 1024 x 1024 bf16 10 against 13.
+//
+// Up to 32 rows of x, a row form where that is expected to take less, or less
+// than the 11 us that the host needs for a split product's two launches (it
+// splits no sum over workgroups and reads the weights once).  Measured on the
+// device, row form against tiles: 8 rows, bf16, 4096 x 4096 8.9 and 10.1, 1024 x
+// 4096 8.3 and 7.4, 1024 x 8192 14.0 and 9.9, 256 x 16384 24.9 and 8.7; 24 rows, 1024
+// x 1024 4.8 and 5.8, 4096 x 4096 12.3 and 11.8, 16384 x 1024 12.2 and 9.2; fp32 4096
+// x 4096 22.3 and 25.9, 1000 x 16000 73.5 and 27.3.
 LinearPlan linear_plan(int M, int N, int kbytes, int dtype) {
     const bool f32 = dtype == DT_F32;
-    if (M <= 16) return {LIN_ROW16, 0, 1, 0};
-    if (M <= 32 && (f32 || (long long)N * kbytes <= 4 << 20)) return {LIN_ROW32, 0, 1, 0};
     const int stages = (kbytes + kStage - 1) / kStage;
     constexpr int CUS = 256;
     auto rounds = [](long long t) { return (t + CUS - 1) / CUS; };
@@ -1073,6 +1085,10 @@ LinearPlan linear_plan(int M, int N, int kbytes, int dtype) {
                               edge_us(form) * (full / CUS + rounds(rest * S)) + parts + (full ? 4.0 : 2.5);
             if (us < best_us) best_us = us, best = {form, (int)full, S, 0};
         }
+    }
+    if (M <= 32) {
+        const double tiles = std::max(best_us, (double)N * kbytes / 4.8e6) + 2.0;
+        if (row_us(M, N, kbytes) <= std::max(tiles, 11.0)) return {M <= 16 ? LIN_ROW16 : LIN_ROW32, 0, 1, 0};
     }
     // Rows whose length is no multiple of 16 bytes cannot go to LDS directly.
     // Passing through registers costs a product about 0.7 of its time more

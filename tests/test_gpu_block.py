@@ -9,7 +9,8 @@ Tolerances, derived before the first run (u = 2^-24, the rounding of fp32):
 - Products of real numbers: K additions, each off by at most 2 u of the partial
   sum (the matrix units may truncate), so |dz| <= 2 (K + 4) u S with S =
   sum |x w| (+ |bias|); scales of 8-bit rows add 3 u |z|.
-- The 8-bit matrix instruction (8-bit rows, 16-bit results, more than 32 rows)
+- The 8-bit matrix instruction (8-bit rows, 16-bit results, more than 32 rows
+  or long sums)
   aligns the products of 8 neighbours of the sum to the largest, p, and cuts
   each below 2^-13 of it (measured with 65536 + 2^e for every e).  The cuts of
   one group are then below 7 * 2^-13 |p|, and |p| is at most the group's share
@@ -113,7 +114,9 @@ def test_whole_numbers_are_exact(mnk, dtype):
 # split over every tile, operands copied to whole stages (K no multiple of 16
 # bytes), and between 17 and 32 rows few and many weights
 PLANS = [(640, 2048, 1024), (1100, 2048, 999), (300, 4096, 1500), (300, 4096, 2048), (40, 520, 8191), (1011, 1500, 515),
-         (24, 1024, 1024), (24, 4100, 2052), (600, 4096, 320), (1500, 1500, 200), (2500, 2048, 131)]
+         (24, 1024, 1024), (24, 4100, 2052), (600, 4096, 320), (1500, 1500, 200), (2500, 2048, 131),
+         # few rows and few weights with long sums: tiles, split
+         (1, 64, 16384), (8, 256, 16383), (16, 1000, 12000), (30, 100, 9001)]
 
 
 @pytest.mark.parametrize("dtype", [F32, F16, BF16, E4M3], ids=str)
