@@ -1062,6 +1062,8 @@ static double row_us(int M, int N, int kbytes) {
 // x 4096 22.3 and 25.9, 1000 x 16000 73.5 and 27.3.
 LinearPlan linear_plan(int M, int N, int kbytes, int dtype) {
     const bool f32 = dtype == DT_F32;
+    const LinearPlan rows{M <= 16 ? LIN_ROW16 : LIN_ROW32, 0, 1, 0};
+    if (M <= 32 && row_us(M, N, kbytes) <= 11.0) return rows;
     const int stages = (kbytes + kStage - 1) / kStage;
     constexpr int CUS = 256;
     auto rounds = [](long long t) { return (t + CUS - 1) / CUS; };
@@ -1088,7 +1090,7 @@ LinearPlan linear_plan(int M, int N, int kbytes, int dtype) {
     }
     if (M <= 32) {
         const double tiles = std::max(best_us, (double)N * kbytes / 4.8e6) + 2.0;
-        if (row_us(M, N, kbytes) <= std::max(tiles, 11.0)) return {M <= 16 ? LIN_ROW16 : LIN_ROW32, 0, 1, 0};
+        if (row_us(M, N, kbytes) <= tiles) return rows;
     }
     // Rows whose length is no multiple of 16 bytes cannot go to LDS directly.
     // Passing through registers costs a product about 0.7 of its time more
