@@ -342,6 +342,8 @@ int ct_conv2d_nchw_depthwise(const void* x, const void* w, float* y,
  * 8-bit rows are e4m3 (OCP: largest value 448, NaN, no infinity) with one
  * fp32 scale a row: the row stands for scale * q.  From a row of values v:
  *   a = max(max_k |v[k]|, 2^-100),  scale = a / 448,  q[k] = rne_e4m3(v[k] / scale)
+ * with scale and the quotient in fp32, each rounded to nearest, so that q is
+ * the same bit for bit on any machine that follows the formula.
  * A row of zeros has scale 2^-100 / 448 and q = 0; a row with a NaN a NaN
  * scale; a row with an infinity (and no NaN) an infinite scale and q = 0 at
  * its finite places, NaN at the others.
@@ -356,11 +358,11 @@ int ct_conv2d_nchw_depthwise(const void* x, const void* w, float* y,
  * must be NULL too.  With a residual, h (the new residual stream, rounded to
  * dtype) may be NULL if it is not wanted; y is made from the unrounded sum.
  * y [M][D] is of out_dtype: CT_F32, CT_F16 or CT_BF16 (scale is NULL), or
- * CT_E4M3 with scale float [M].  Sums are fp32; a row of zeros with eps = 0 is
- * NaN, and one whose squares pass the range of fp32 zeros, as the formula says
- * in fp32.  h and y may each be exactly x
- * or residual (same pointer, stride and type), not the same one; no other
- * overlap.  Errors: CT_ERR_INVALID_ARG for M < 0, D < 1, a NULL or misaligned pointer,
+ * CT_E4M3 with scale float [M]: the 8-bit rows of y's fp32 values.  Sums are
+ * fp32; a row of zeros with eps = 0 is NaN, and one whose squares pass the
+ * range of fp32 zeros, as the formula says in fp32.  h and y may each be
+ * exactly x or residual (same pointer, stride and type), not the same one; no
+ * other overlap.  Errors: CT_ERR_INVALID_ARG for M < 0, D < 1, a NULL or misaligned pointer,
  * a stride below D, an unknown dtype, h without residual, scale missing (or
  * given without CT_E4M3), or eps negative or not finite; CT_ERR_HIP on a
  * launch failure.  Asynchronous on `stream`. */

@@ -2,26 +2,31 @@
 // the 8-bit quantization of rows.
 //
 //   h = x + residual                      (fp32; stored rounded to x's type)
-//   y = h * r * gain,  r = 1 / sqrt(mean h^2 + eps)      (norm; else y = h)
+//   y = (h * gain) * r,  r = 1 / sqrt(mean h^2 + eps)      (norm; else y = h)
 //   e4m3:  a = max(max |y|, 2^-100),  scale = a / 448,  q = rne(y / scale)
 //
-// The row factor r cancels out of q: y / scale = t * 448 / max |t| with
-// t = h * gain.  So the sum of squares and the maximum of |t| are reduced
-// together, over one reading of the row, which stays in registers, and q
-// takes two roundings of 32 bits (t, and its product with 448 / max |t|)
-// before its own.  The quotient form y = t * r, q = y * (448 / a) is kept
-// for the rows where 448 / max |t| could leave the range of fp32 (a or
-// max |t| below 2^-100, or not finite).
+// The sum of squares and the maximum of |t|, t = h * gain, are reduced
+// together, over one reading of the row, which stays in registers: max |y| is
+// max |t| times r, rounded, since rounding keeps the order.
+//
+// y, scale and the quotient are fp32, each rounded to nearest, so the codes of
+// a norm are those of its fp32 values.  The quotient has to be rounded as one:
+// rows of two-byte types put many of them half way between two codes, and a
+// product with a rounded 448 / a in its place moves all of a row's the same
+// way (0.1% of a bf16 row's codes).  A product with 1 / scale and corrections by
+// the remainder (Divisor, below) gives the quotient's bits in 3 or 5 operations
+// (16384 x 8192 fp16 70 us, with a division an element 85).
 //
 // The maximum is taken over the bit patterns of |t| as unsigned integers:
 // the order is that of the values, infinity above every finite value and NaN
 // above infinity, so a NaN anywhere in a row reaches its scale.
 //
-// Bound by memory: about 5 operations an element.  A row is held by TPR
+// Bound by memory: about 10 operations an element.  A row is held by TPR
 // threads, 16 bytes of the input's type a load and C loads a thread, all
 // issued before the first is used.  Measured: rmsnorm of 8192 x 8192 bf16 with a
-// residual 95.0 us (537 MB, 5.65 TB/s; a device copy moves 5.1 to 5.2), 16384 x
-// 8192 fp16 to e4m3 68.6 us (403 MB, 5.9 TB/s); one row of 4096 3.2 us on the device.
+// residual 95.0 us (537 MB, 5.65 TB/s; a device copy moves 5.1 to 5.2), to e4m3 92
+// (5.1 TB/s), 16384 x 8192 fp16 to e4m3 68.6 us (403 MB, 5.9 TB/s); one row of
+// 4096 3.6 us on the device.
 #include "ct_device.hpp"
 #include "block_kernels.hpp"
 
@@ -103,9 +108,43 @@ __device__ __forceinline__ void store_e4m3(char* p, int n, const float (&f)[V]) 
 
 __device__ __forceinline__ int elem_bytes(int dt) { return dt == DT_F32 ? 4 : dt == OUT_E4M3 ? 1 : 2; }
 
-// What a row's statistics give: every element is (t * m1) * m2.
+// Quotients by a row's scale s, rounded to nearest.  With inv = 1 / s rounded to
+// nearest, v * inv is off by at most 1.5 steps; adding the remainder times inv
+// leaves the quotient's neighbour on either side or the quotient itself, and
+// from there a second such step rounds it correctly (Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990).  The
+// remainders are exact while the products of their last places are normal: for
+// s between 2^-80 and 2^100 they are wherever the quotient is 2^-11 or more,
+// and below that its code is a zero whatever its last bits.  Rows outside
+// (zeros and nearly so, infinities, NaN) divide.
+// A row of a two-byte type that is brought to 8 bits as it is needs one step
+// (STEPS): it gives the quotient for all pairs of 11-bit significands of v and
+// of the row's maximum, and exponents only scale them (16384 x 8192 fp16 71.4
+// us with two steps, 70.2 with one).
+template <int STEPS>
+struct Divisor {
+    float s, inv;
+    bool usual;
+    __device__ __forceinline__ explicit Divisor(float scale)
+        : s(scale), inv(1.0f / scale), usual(scale >= 0x1p-80f && scale <= 0x1p100f) {}
+    // The remainder is taken negative so that a zero keeps its sign.
+    __device__ __forceinline__ float near(float v) const {
+        float q = v * inv;
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) q = fmaf(-fmaf(q, s, -v), inv, q);
+        return q;
+    }
+    __device__ __forceinline__ float any(float v) const { return v / s; }
+};
+
+template <int DT, bool NORM>
+constexpr int quotient_steps() {
+    return !NORM && DT != DT_F32 ? 1 : 2;
+}
+
+// What a row's statistics give: y = t * r, and the scale of 8-bit output.
 struct RowFactors {
-    float m1, m2;
+    float r, scale;
 };
 
 // ss: the sum of squares, tbits: the bits of max |t|.
@@ -113,12 +152,11 @@ template <bool NORM>
 __device__ __forceinline__ RowFactors row_factors(float ss, uint32_t tbits, int D, int out_dt, float eps, float* scale) {
     const float r = NORM ? 1.0f / sqrtf(ss / (float)D + eps) : 1.0f;
     if (out_dt != OUT_E4M3) return {r, 1.0f};
-    const float tmax = __uint_as_float(tbits);
-    const float a0 = r * tmax;
+    const float a0 = r * __uint_as_float(tbits);
     const float a = a0 < kFloor ? kFloor : a0;  // NaN stays
-    if (scale) *scale = a / kE4m3Max;
-    if (tmax >= kFloor && a0 >= kFloor) return {kE4m3Max / tmax, 1.0f};
-    return {r, kE4m3Max / a};
+    const float s = a / kE4m3Max;
+    if (scale) *scale = s;
+    return {r, s};
 }
 
 // Reductions over the TPR threads of a row (whole waves): the sum of squares
@@ -210,18 +248,33 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void rows_kernel(RowsParams 
     reduce_row<TPR>(ss, tb);
     const RowFactors f = row_factors<NORM>(ss, tb, p.D, p.out_dt, p.eps, lt == 0 && p.scale ? p.scale + row : nullptr);
     char* y = p.y + row * p.ldy;
-    const int oes = elem_bytes(p.out_dt);
+    auto put = [&](auto store) {  // store(address, elements, values)
+        const int oes = elem_bytes(p.out_dt);
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int e = (c * TPR + lt) * V;
-        float o[V];
+        for (int c = 0; c < C; ++c) {
+            const int e = (c * TPR + lt) * V;
+            float o[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = h[c][i] * f.m1 * f.m2;
-        char* yo = y + (long long)e * oes;
-        if (p.out_dt == OUT_E4M3)
-            store_e4m3<V>(yo, p.D - e, o);
+            for (int i = 0; i < V; ++i) o[i] = NORM ? h[c][i] * f.r : h[c][i];
+            store(y + (long long)e * oes, p.D - e, o);
+        }
+    };
+    if (p.out_dt == OUT_E4M3) {
+        const Divisor<quotient_steps<DT, NORM>()> d(f.scale);
+        if (d.usual)
+            put([&](char* at, int n, float (&o)[V]) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) o[i] = d.near(o[i]);
+                store_e4m3<V>(at, n, o);
+            });
         else
-            store_vec<V>(yo, p.D - e, p.out_dt, o);
+            put([&](char* at, int n, float (&o)[V]) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) o[i] = d.any(o[i]);
+                store_e4m3<V>(at, n, o);
+            });
+    } else {
+        put([&](char* at, int n, const float (&o)[V]) { store_vec<V>(at, n, p.out_dt, o); });
     }
 }
 
@@ -273,6 +326,7 @@ __global__ __launch_bounds__(1024) void rows_long_kernel(RowsParams p) {
         row_factors<NORM>(ss, tb, p.D, p.out_dt, p.eps, threadIdx.x == 0 && p.scale ? p.scale + row : nullptr);
     char* y = p.y + row * p.ldy;
     const int oes = elem_bytes(p.out_dt);
+    const Divisor<quotient_steps<DT, NORM>()> d(f.scale);
     for (long long e = (long long)threadIdx.x * V; e < p.D; e += TPR * V) {
         const int n = (int)((long long)p.D - e < V ? (long long)p.D - e : V);
         float h[V], o[V];
@@ -280,11 +334,14 @@ __global__ __launch_bounds__(1024) void rows_long_kernel(RowsParams p) {
         if (p.h) store_vec<V>(p.h + row * p.ldh + e * ES, n, DT, h);
         times_gain(e, h);
 #pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = h[i] * f.m1 * f.m2;
-        if (p.out_dt == OUT_E4M3)
+        for (int i = 0; i < V; ++i) o[i] = NORM ? h[i] * f.r : h[i];
+        if (p.out_dt == OUT_E4M3) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) o[i] = d.usual ? d.near(o[i]) : d.any(o[i]);
             store_e4m3<V>(y + e * oes, n, o);
-        else
+        } else {
             store_vec<V>(y + e * oes, n, p.out_dt, o);
+        }
     }
 }
 
