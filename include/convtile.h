@@ -426,11 +426,11 @@ int ct_linear_fwd(const void* x, long long ldx, const void* w, long long ldw,
 /* The same on 8-bit rows: x [M][K] and w [N][K] are CT_E4M3 with row scales
  * xs [M] and ws [N]:
  *   z[m][n] = xs[m] * ws[n] * sum_{k<K} x[m][k] * w[n][k]
- * With CT_F32 output, and for up to 32 rows of x where the sizes do not call
- * for tiles, the operands are widened to fp16, exactly, and the sums are fp32.
- * Otherwise the 8-bit matrix instruction is used, which aligns each 8
- * neighbouring products to the largest of them and cuts what lies 2^-13 below
- * it: about 1.5e-5 of a sum's size on normally distributed rows, 1/130 of the
+ * With CT_F32 output, and for up to 32 rows of x, the operands are widened to
+ * fp16, exactly, and the sums are fp32.  Otherwise (16-bit results of more
+ * rows) the 8-bit matrix instruction is used, which aligns each 8 neighbouring
+ * products to the largest of them and cuts what lies 2^-13 below it: about
+ * 1.5e-5 of a sum's size on normally distributed rows, 1/130 of the
  * rounding to bf16 and 1/16 of that to fp16. */
 int ct_linear_q8_fwd(const void* x, long long ldx, const float* xs,
                      const void* w, long long ldw, const float* ws,

@@ -38,9 +38,13 @@ typedef __attribute__((address_space(3))) void lds_void_t;
 // measured, with the cut the same on the older 8-bit instructions): sums off by
 // 1.5e-5 of their size in the 2-norm on normally distributed rows, whatever K.
 // That is 1/130 of the rounding of a bf16 result and 1/16 of an fp16 one, for
-// twice the rate.  DT_E4M3_WIDE widens the operands to fp16, exactly, and
-// takes its instruction, whose sums keep fp32: for fp32 results, and for the
-// row forms, which the weights' reading bounds anyway.
+// twice the rate; a cut is at most 1/512 of what rounding a factor to e4m3 may
+// have moved the group's largest product by.  DT_E4M3_WIDE widens the operands
+// to fp16, exactly, and takes its instruction, whose sums keep fp32: for fp32
+// results (4096 x 8192 x 4096 221 us, 112 to bf16 on the other), and for up to 32
+// rows of x, whatever form the sizes choose, so that a token's sums do not
+// depend on the layer's (the weights' reading bounds those products: tiles of
+// 8 x 256 x 16384 8.8 us, 8.0 on the 8-bit instruction, 32 x 4096 x 4096 8.8 and 8.6).
 enum { DT_E4M3 = 3, DT_E4M3_WIDE = 4 };
 enum { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SILU = 4 };
 
@@ -1126,8 +1130,8 @@ hipError_t launch_linear(LinearPlan plan, LinearParams p, int dtype, bool aligne
         case DT_F16: return launch_dt<DT_F16>(plan, p, aligned, stream);
         case DT_BF16: return launch_dt<DT_BF16>(plan, p, aligned, stream);
         default:
-            return p.out_dt == DT_F32 ? launch_dt<DT_E4M3_WIDE>(plan, p, aligned, stream)
-                                      : launch_dt<DT_E4M3>(plan, p, aligned, stream);
+            return p.out_dt == DT_F32 || p.M <= 32 ? launch_dt<DT_E4M3_WIDE>(plan, p, aligned, stream)
+                                                   : launch_dt<DT_E4M3>(plan, p, aligned, stream);
     }
 }
 
