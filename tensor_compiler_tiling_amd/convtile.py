@@ -348,18 +348,29 @@ def _row_ptr(t) -> Optional[int]:
     return t if t is None or isinstance(t, int) else t.data_ptr()
 
 
+def _counts(**sizes) -> None:
+    """ctypes keeps the low 32 bits of an int: counts that need more are refused
+    here, before the library would answer for others."""
+    for name, n in sizes.items():
+        if not -(1 << 31) <= n < 1 << 31:
+            raise ValueError(f"{name} = {n} does not fit 32 bits")
+
+
 def ct_rmsnorm_fwd(x, ldx, residual, ldr, gain, h, ldh, y, ldy, scale, M, D, dtype, out_dtype, eps=1e-6,
                    stream=None) -> int:
+    _counts(M=M, D=D)
     return _load().ct_rmsnorm_fwd(_row_ptr(x), ldx, _row_ptr(residual), ldr, _ptr(gain), _row_ptr(h), ldh,
                                   _row_ptr(y), ldy, _ptr(scale), M, D, dtype, out_dtype, eps, _stream(stream))
 
 
 def ct_quantize_rows(x, ldx, q, ldq, scale, M, D, dtype, stream=None) -> int:
+    _counts(M=M, D=D)
     return _load().ct_quantize_rows(_row_ptr(x), ldx, _row_ptr(q), ldq, _ptr(scale), M, D, dtype, _stream(stream))
 
 
 def ct_linear_fwd(x, ldx, w, ldw, y, ldy, M, N, K, dtype, out_dtype, epi: Optional[ct_linear_epilogue] = None,
                   workspace=None, workspace_bytes=0, stream=None) -> int:
+    _counts(M=M, N=N, K=K)
     return _load().ct_linear_fwd(_row_ptr(x), ldx, _row_ptr(w), ldw, _row_ptr(y), ldy, M, N, K, dtype, out_dtype,
                                  ctypes.addressof(epi) if epi is not None else None, _ptr(workspace),
                                  workspace_bytes, _stream(stream))
@@ -367,12 +378,14 @@ def ct_linear_fwd(x, ldx, w, ldw, y, ldy, M, N, K, dtype, out_dtype, epi: Option
 
 def ct_linear_q8_fwd(x, ldx, xs, w, ldw, ws, y, ldy, M, N, K, out_dtype, epi: Optional[ct_linear_epilogue] = None,
                      workspace=None, workspace_bytes=0, stream=None) -> int:
+    _counts(M=M, N=N, K=K)
     return _load().ct_linear_q8_fwd(_row_ptr(x), ldx, _ptr(xs), _row_ptr(w), ldw, _ptr(ws), _row_ptr(y), ldy, M, N,
                                     K, out_dtype, ctypes.addressof(epi) if epi is not None else None,
                                     _ptr(workspace), workspace_bytes, _stream(stream))
 
 
 def ct_linear_workspace_bytes(M, N, K, dtype) -> int:
+    _counts(M=M, N=N, K=K)
     return _load().ct_linear_workspace_bytes(M, N, K, dtype)
 
 
@@ -712,9 +725,11 @@ def _first(name: str, t):
     index, shape = t.get_device(), t.shape
     if len(shape) != 2:
         raise ValueError(f"{name} must have two dimensions")
+    M, D = shape
+    if (M | D) >> 31:
+        raise ValueError(f"{name}: {M} rows of {D} do not fit 32 bits")
     if index < 0:
         raise ValueError(f"{name} must be a GPU tensor")
-    M, D = shape
     ld, step = t.stride()
     if M <= 1:
         ld = D  # a single row has no stride to speak of
@@ -840,6 +855,8 @@ def _product(x, xs, w, ws, bias, act, gate, residual, out_dtype, out, stream):
     N, K2 = w.shape if w.dim() == 2 else (0, 0)
     if K != K2:
         raise ValueError(f"x has rows of {K} and w of {K2}")
+    if N >> 31:
+        raise ValueError(f"w: {N} rows do not fit 32 bits")
     xt = x.dtype
     if xs is None:
         dtype = _code(xt)

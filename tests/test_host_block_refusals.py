@@ -1,0 +1,50 @@
+"""More refusals of the transformer-block entry points, before any HIP call:
+the addresses here are never read."""
+import os
+
+import pytest
+import torch
+
+from tensor_compiler_tiling_amd import convtile as ct
+
+P = 1 << 20  # an aligned address that no call here reads
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not os.path.exists(ct.LIB_PATH):
+        from tensor_compiler_tiling_amd import build
+        build.build()
+
+
+LIN = dict(x=P, ldx=64, w=2 * P, ldw=64, y=3 * P, ldy=32, M=4, N=32, K=64, dtype=ct.CT_BF16, out_dtype=ct.CT_BF16, epi=None,
+           workspace=None, workspace_bytes=0, stream=0)
+Q8 = dict(x=P, ldx=64, xs=P, w=2 * P, ldw=64, ws=P, y=3 * P, ldy=32, M=4, N=32, K=64, out_dtype=ct.CT_BF16, epi=None,
+          workspace=None, workspace_bytes=0, stream=0)
+NORM = dict(x=P, ldx=64, residual=2 * P, ldr=64, gain=P, h=3 * P, ldh=64, y=4 * P, ldy=64, scale=None, M=4, D=64,
+            dtype=ct.CT_BF16, out_dtype=ct.CT_BF16, eps=1e-6, stream=0)
+QUANT = dict(x=P, ldx=64, q=2 * P, ldq=64, scale=P, M=4, D=64, dtype=ct.CT_BF16, stream=0)
+CALLS = {"linear": (ct.ct_linear_fwd, LIN, "MNK"), "linear_q8": (ct.ct_linear_q8_fwd, Q8, "MNK"),
+         "rmsnorm": (ct.ct_rmsnorm_fwd, NORM, "MD"), "quantize_rows": (ct.ct_quantize_rows, QUANT, "MD"),
+         "workspace": (ct.ct_linear_workspace_bytes, dict(M=4, N=32, K=64, dtype=ct.CT_BF16), "MNK")}
+
+
+@pytest.mark.parametrize("n", [1 << 31, 1 << 32, (1 << 32) + 64, (1 << 40) + 1, -(1 << 32)])
+@pytest.mark.parametrize("call", list(CALLS))
+def test_counts_past_32_bits_are_not_cut(call, n):
+    """2^32 rows would be none, and 2^32 + 64 elements 64."""
+    f, args, names = CALLS[call]
+    for name in names:
+        with pytest.raises(ValueError, match="32 bits"):
+            f(**{**args, name: n})
+
+
+@pytest.mark.parametrize("shape", [(1 << 32, 1), ((1 << 32) + 3, 1), (1, (1 << 32) + 1), (1 << 31, 1)], ids=str)
+def test_helpers_refuse_counts_past_32_bits(shape):
+    x = torch.empty(shape, dtype=torch.bfloat16, device="meta")
+    q = torch.empty(shape, dtype=torch.float8_e4m3fn, device="meta")
+    s = torch.empty(1, device="meta")
+    for call in (lambda: ct.rmsnorm(x), lambda: ct.quantize_rows(x), lambda: ct.linear(x, x[:1]),
+                 lambda: ct.linear_q8(q, s, q[:1], s)):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
