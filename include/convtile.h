@@ -364,8 +364,9 @@ int ct_conv2d_nchw_depthwise(const void* x, const void* w, float* y,
  * exactly x or residual (same pointer, stride and type), not the same one; no
  * other overlap.  Errors: CT_ERR_INVALID_ARG for M < 0, D < 1, a NULL or misaligned pointer,
  * a stride below D, an unknown dtype, h without residual, scale missing (or
- * given without CT_E4M3), or eps negative or not finite; CT_ERR_HIP on a
- * launch failure.  Asynchronous on `stream`. */
+ * given without CT_E4M3), h or y at the address of an input with another
+ * stride or type, or eps negative or not finite; CT_ERR_HIP on a launch
+ * failure.  Asynchronous on `stream`. */
 int ct_rmsnorm_fwd(const void* x, long long ldx, const void* residual, long long ldr,
                    const float* gain, void* h, long long ldh, void* y, long long ldy,
                    float* scale, int M, int D, int dtype, int out_dtype, float eps,
@@ -414,7 +415,8 @@ typedef struct ct_linear_epilogue {
  * time, need one each.
  * Errors: CT_ERR_INVALID_ARG for M < 0, N or K < 1, a NULL or misaligned
  * pointer, a stride below the row's length, an unknown dtype or activation,
- * y equal to x or w, or a workspace that is too small; CT_ERR_UNSUPPORTED for
+ * y equal to x or w, or to gate or residual with another stride, or a
+ * workspace that is too small; CT_ERR_UNSUPPORTED for
  * M, N or a row's bytes above 2^30, x or w rows more than 8 MiB apart, or
  * results that one launch cannot cover (2^23 tiles of 64 x 64 to 256 x 256,
  * chosen by the sizes); CT_ERR_HIP on a launch failure.  Asynchronous on `stream`. */

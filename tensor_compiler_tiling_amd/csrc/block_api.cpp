@@ -35,6 +35,15 @@ int check_floats(const char* name, const float* p) {
     return CT_OK;
 }
 
+// An output on an input's place: every element must fall on the one it is made
+// from (one type, and one stride where there are rows to be apart), or a row's
+// results land on another's inputs before they are read.
+int check_in_place(const char* out, const void* o, long long ldo, int odt, const char* in, const void* i, long long ldi,
+                   int idt, int M) {
+    if (!i || o != i || (odt == idt && (M == 1 || ldo == ldi))) return CT_OK;
+    return fail(CT_ERR_INVALID_ARG, "%s is in the place of %s with another type or stride", out, in);
+}
+
 bool aligned16(const void* p, long long ld_bytes) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld_bytes % 16 == 0;
 }
@@ -48,11 +57,16 @@ int rows_call(const void* x, long long ldx, const void* residual, long long ldr,
     if (norm && !(eps >= 0.0f && eps <= FLT_MAX)) return fail(CT_ERR_INVALID_ARG, "eps must be finite and not negative");
     if (h && !residual) return fail(CT_ERR_INVALID_ARG, "h is the sum with residual, which is NULL");
     if (M == 0) return CT_OK;
+    const char* yname = norm ? "y" : "q";
     int st = check_matrix("x", x, ldx, D, dtype);
-    if (st == CT_OK) st = check_matrix(norm ? "y" : "q", y, ldy, D, out_dtype);
+    if (st == CT_OK) st = check_matrix(yname, y, ldy, D, out_dtype);
     if (st == CT_OK && residual) st = check_matrix("residual", residual, ldr, D, dtype);
     if (st == CT_OK && h) st = check_matrix("h", h, ldh, D, dtype);
     if (st == CT_OK && gain) st = check_floats("gain", gain);
+    if (st == CT_OK) st = check_in_place(yname, y, ldy, out_dtype, "x", x, ldx, dtype, M);
+    if (st == CT_OK) st = check_in_place(yname, y, ldy, out_dtype, "residual", residual, ldr, dtype, M);
+    if (st == CT_OK && h) st = check_in_place("h", h, ldh, dtype, "x", x, ldx, dtype, M);
+    if (st == CT_OK && h) st = check_in_place("h", h, ldh, dtype, "residual", residual, ldr, dtype, M);
     if (st == CT_OK && h == y) return fail(CT_ERR_INVALID_ARG, "h and y must not be the same");
     if (st != CT_OK) return st;
     if (out_dtype == CT_E4M3) {
@@ -106,6 +120,8 @@ int linear_call(const void* x, long long ldx, const float* xs, const void* w, lo
     if (st == CT_OK && (y == x || y == w)) return fail(CT_ERR_INVALID_ARG, "y must not be x or w");
     if (st == CT_OK && ep.gate) st = check_matrix("gate", ep.gate, ep.ldg, N, out_dtype);
     if (st == CT_OK && ep.residual) st = check_matrix("residual", ep.residual, ep.ldr, N, out_dtype);
+    if (st == CT_OK) st = check_in_place("y", y, ldy, out_dtype, "gate", ep.gate, ep.ldg, out_dtype, M);
+    if (st == CT_OK) st = check_in_place("y", y, ldy, out_dtype, "residual", ep.residual, ep.ldr, out_dtype, M);
     if (st == CT_OK && ep.bias) st = check_floats("bias", ep.bias);
     if (st == CT_OK && q8) st = check_floats("xs", xs);
     if (st == CT_OK && q8) st = check_floats("ws", ws);

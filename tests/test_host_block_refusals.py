@@ -48,3 +48,33 @@ def test_helpers_refuse_counts_past_32_bits(shape):
                  lambda: ct.linear_q8(q, s, q[:1], s)):
         with pytest.raises(ValueError, match="32 bits"):
             call()
+
+
+@pytest.mark.parametrize("over", [
+    dict(y=P, out_dtype=ct.CT_E4M3, scale=P), dict(y=2 * P, out_dtype=ct.CT_E4M3, scale=P),
+    dict(y=P, out_dtype=ct.CT_F32), dict(y=2 * P, out_dtype=ct.CT_F16),
+    dict(y=P, ldy=72), dict(y=2 * P, ldy=128), dict(h=P, ldh=65), dict(h=2 * P, ldr=66),
+    dict(y=P, ldy=72, M=2), dict(y=P, out_dtype=ct.CT_F32, M=1),
+], ids=str)
+def test_rmsnorm_refuses_to_write_over_rows_it_has_not_read(over):
+    assert ct.ct_rmsnorm_fwd(**{**NORM, **over}) == ct.CT_ERR_INVALID_ARG
+    assert "in the place of" in ct.ct_last_error()
+
+
+@pytest.mark.parametrize("dtype", [ct.CT_F32, ct.CT_F16, ct.CT_BF16])
+@pytest.mark.parametrize("M", [1, 4])
+def test_quantize_rows_refuses_to_write_over_its_input(M, dtype):
+    assert ct.ct_quantize_rows(**{**QUANT, "q": P, "M": M, "dtype": dtype, "ldq": 128}) == ct.CT_ERR_INVALID_ARG
+    assert "in the place of" in ct.ct_last_error()
+
+
+@pytest.mark.parametrize("ep", [dict(gate=3 * P, ldg=40), dict(residual=3 * P, ldr=33),
+                                dict(gate=3 * P, ldg=32, residual=3 * P, ldr=64)], ids=str)
+def test_products_refuse_a_gate_or_residual_in_place_with_another_stride(ep):
+    e = ct.ct_linear_epilogue()
+    for k, v in ep.items():
+        setattr(e, k, v)
+    assert ct.ct_linear_fwd(**{**LIN, "epi": e}) == ct.CT_ERR_INVALID_ARG
+    assert "in the place of" in ct.ct_last_error()
+    assert ct.ct_linear_q8_fwd(**{**Q8, "epi": e}) == ct.CT_ERR_INVALID_ARG
+    assert "in the place of" in ct.ct_last_error()
