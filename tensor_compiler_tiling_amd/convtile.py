@@ -345,7 +345,16 @@ def ct_broadcast_chain(prog, a0, a1, a2, a3, x, out, out_dtype, outer, P, inner,
 
 def _row_ptr(t) -> Optional[int]:
     """The address of a matrix whose rows may lie apart (or a device pointer)."""
-    return t if t is None or isinstance(t, int) else t.data_ptr()
+    if t is None or isinstance(t, int):
+        return t
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"expected a torch tensor or a device pointer, got {type(t)}")
+    if not t.is_cuda:
+        raise ValueError("tensor must be on the GPU")
+    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("the elements of a row must be contiguous")
+    return t.data_ptr()
 
 
 def _counts(**sizes) -> None:

@@ -78,3 +78,14 @@ def test_products_refuse_a_gate_or_residual_in_place_with_another_stride(ep):
     assert "in the place of" in ct.ct_last_error()
     assert ct.ct_linear_q8_fwd(**{**Q8, "epi": e}) == ct.CT_ERR_INVALID_ARG
     assert "in the place of" in ct.ct_last_error()
+
+
+@pytest.mark.parametrize("call,name", [(c, n) for c, (_, args, _) in CALLS.items() for n in
+                                       ("x", "w", "y", "q", "h", "residual", "xs", "ws", "gain", "scale") if args.get(n)])
+def test_raw_entry_points_refuse_host_tensors(call, name):
+    """A host address would be read by the kernel."""
+    f, args, _ = CALLS[call]
+    with pytest.raises(ValueError, match="on the GPU"):
+        f(**{**args, name: torch.zeros(4, 64)})
+    with pytest.raises(TypeError):
+        f(**{**args, name: [0.0] * 256})
