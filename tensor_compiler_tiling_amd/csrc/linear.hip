@@ -129,10 +129,37 @@ __device__ __forceinline__ float sigmoid_times(float z, float u) {
     return z * __builtin_amdgcn_rcpf(1.0f + dev_exp(-u));
 }
 
+// erfc(a / sqrt 2) / 2, the normal distribution's tail beyond a >= 0, to a few
+// units in the last place of a value that falls as exp(-a^2 / 2): that exponential
+// times a polynomial in t = 1 / (1 + 0.3 a) (the form of Hastings, "Approximations
+// for Digital Computers", 1955).  The coefficients are a least-squares fit of
+// the relative error, reweighted until it is even: 1.5e-7 over 0 <= a <= 14.
+// 4096 x 8192 x 4096 bf16 with gelu 239 us (249 with the device library's erff, whose
+// 1 + erf loses the tail, 262 with its erfcf).
+__device__ __forceinline__ float normal_tail(float a) {
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.3f, a, 1.0f));
+    float p = 0.0356747732f;
+    p = fmaf(p, t, -0.157203078f);
+    p = fmaf(p, t, 0.206353515f);
+    p = fmaf(p, t, -0.053683646f);
+    p = fmaf(p, t, 0.128561631f);
+    p = fmaf(p, t, 0.0999134928f);
+    p = fmaf(p, t, 0.120753959f);
+    p = fmaf(p, t, 0.119629301f);
+    return p * t * __builtin_amdgcn_exp2f(-0.72134752f * (a * a));  // log2(e) / 2
+}
+
+// z times the normal distribution function.  For negative z that is its tail:
+// as (1 + erf) / 2 the digits would cancel.
+__device__ __forceinline__ float gelu(float z) {
+    const float q = normal_tail(fabsf(z));
+    return z * (z < 0.0f ? q : 1.0f - q);
+}
+
 template <int ACT>
 __device__ __forceinline__ float activated(float z) {
     if constexpr (ACT == ACT_RELU) return z < 0.0f ? 0.0f : z;  // NaN stays
-    if constexpr (ACT == ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
+    if constexpr (ACT == ACT_GELU) return gelu(z);
     // 0.5 (1 + tanh u) = 1 / (1 + exp(-2 u)), u = sqrt(2 / pi) (z + 0.044715 z^3)
     if constexpr (ACT == ACT_GELU_TANH) return sigmoid_times(z, 1.5957691f * fmaf(0.044715f * z * z, z, z));
     if constexpr (ACT == ACT_SILU) return sigmoid_times(z, z);
