@@ -124,9 +124,22 @@ __device__ __forceinline__ floatx4 mma16(uint4v a0, uint4v a1, uint4v b0, uint4v
 }
 
 // ---------------------------------------------------------------- epilogue --
-// exp and the reciprocal run on the hardware units, about 1 ulp each.
+// z / (1 + exp(-u)); exp and the reciprocal run on the hardware units, about 1 ulp
+// each.  WHOLE: with e = exp(-|u|) it is z e / (1 + e) for negative u, so a small
+// result keeps its digits until e leaves the range of fp32 (2^-126), and the
+// exponent's rounding, |u| 2^-24 of the result by itself, is carried along.
+// Not WHOLE: neither, for 16-bit results, where that rounding is below 2^-17 of
+// the result, and results below 2^-119 become zeros (8192 x 8192 x 1024 bf16 with
+// silu 140 us, 151 WHOLE).
+template <bool WHOLE>
 __device__ __forceinline__ float sigmoid_times(float z, float u) {
-    return z * __builtin_amdgcn_rcpf(1.0f + dev_exp(-u));
+    if constexpr (!WHOLE) return z * __builtin_amdgcn_rcpf(1.0f + dev_exp(-u));
+    const float t = fmaxf(-fabsf(u), -128.0f);  // exp2 of it is 0, and infinities have no remainder
+    const float hi = t * 1.44269504f;           // log2(e) to 24 bits, and the rest of it
+    const float lo = fmaf(t, 1.925963e-8f, fmaf(t, 1.44269504f, -hi));
+    const float e0 = __builtin_amdgcn_exp2f(hi);
+    const float e = fmaf(e0, lo * 0.69314718f, e0);
+    return z * (u < 0.0f ? e : 1.0f) * __builtin_amdgcn_rcpf(1.0f + e);
 }
 
 // erfc(a / sqrt 2) / 2, the normal distribution's tail beyond a >= 0, to a few
@@ -156,13 +169,13 @@ __device__ __forceinline__ float gelu(float z) {
     return z * (z < 0.0f ? q : 1.0f - q);
 }
 
-template <int ACT>
+template <int ACT, bool WHOLE>
 __device__ __forceinline__ float activated(float z) {
     if constexpr (ACT == ACT_RELU) return z < 0.0f ? 0.0f : z;  // NaN stays
     if constexpr (ACT == ACT_GELU) return gelu(z);
     // 0.5 (1 + tanh u) = 1 / (1 + exp(-2 u)), u = sqrt(2 / pi) (z + 0.044715 z^3)
-    if constexpr (ACT == ACT_GELU_TANH) return sigmoid_times(z, 1.5957691f * fmaf(0.044715f * z * z, z, z));
-    if constexpr (ACT == ACT_SILU) return sigmoid_times(z, z);
+    if constexpr (ACT == ACT_GELU_TANH) return sigmoid_times<WHOLE>(z, 1.5957691f * fmaf(0.044715f * z * z, z, z));
+    if constexpr (ACT == ACT_SILU) return sigmoid_times<WHOLE>(z, z);
     return z;
 }
 
@@ -182,7 +195,7 @@ template <int V>
 __device__ __forceinline__ void activate(float (&z)[V], int act) {
     with_activation(act, [&](auto a) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) z[i] = activated<decltype(a)::value>(z[i]);
+        for (int i = 0; i < V; ++i) z[i] = activated<decltype(a)::value, true>(z[i]);
     });
 }
 
@@ -840,7 +853,7 @@ __global__ __launch_bounds__(KG* WM* WN * 64) void linear_tile_kernel(LinearPara
                     turned(row0 + t * RPS, v);
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        v[i] = activated<ACT>(DT == DT_E4M3 ? fmaf(v[i] * now.xs[t], cs[i], cb[i]) : v[i] + cb[i]);
+                        v[i] = activated<ACT, false>(DT == DT_E4M3 ? fmaf(v[i] * now.xs[t], cs[i], cb[i]) : v[i] + cb[i]);
                     if (gw) {
                         halves(now.g[t], f);
 #pragma unroll

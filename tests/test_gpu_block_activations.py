@@ -58,6 +58,25 @@ def test_gelu_keeps_its_digits_in_the_negative_tail(rows):
     assert worst <= 1.0
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("rows", ROWS)
+def test_sigmoids_keep_their_digits_in_the_negative_tail(rows, act):
+    """z / (1 + exp(-v)), v = z (silu) or sqrt(8 / pi) (z + 0.044715 z^3), taken as
+    z e / (1 + e) with e = exp(v): e to 6 u beside what v itself is off by (0 for
+    silu; two constants and five operations, 5 u |v|, for gelu_tanh), the
+    reciprocal 2 u, two products and a sum 3 u, one for the rest.  Below exp(-87)
+    the exponential's unit gives zeros: 2^-126 |z|."""
+    z = -torch.linspace(0.01, 100.0 if act == "silu" else 11.0, 600, device=DEV)
+    y = of_points(act, z, rows)
+    zd = z.double()
+    v = zd if act == "silu" else (8 / torch.pi) ** 0.5 * (zd + 0.044715 * zd ** 3)
+    ref = zd * torch.exp(v) / (1 + torch.exp(v))
+    tol = (12 + (0 if act == "silu" else 5 * v.abs())) * U * ref.abs() + 2.0 ** -126 * zd.abs()
+    worst = float(((y - ref).abs() / tol).max())
+    say(f"  {act}, {rows} rows: {worst:.3f} of the tolerance")
+    assert worst <= 1.0
+
+
 @pytest.mark.parametrize("rows", ROWS)
 def test_activations_of_large_and_special_values(rows):
     inf, nan = float("inf"), float("nan")
