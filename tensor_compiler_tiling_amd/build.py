@@ -5,10 +5,10 @@
 Every source under csrc/ is compiled with hipcc for gfx950 into _build/ and
 linked into tensor_compiler_tiling_amd/libconvtile.so.
 
-build_host_check() also compiles every source host-only (no device code)
-with AddressSanitizer and UndefinedBehaviorSanitizer and links it with
-tests/sanitize/host_check.cpp into _build/asan/host_check, a CPU-only check
-of the runtime's host code.
+build_host_check() also compiles the host sources (csrc/*.cpp) with
+AddressSanitizer and UndefinedBehaviorSanitizer on their host side and links
+them with tests/sanitize/host_check.cpp and block_check.cpp into
+_build/asan/, CPU-only checks of the library's host code.
 """
 from __future__ import annotations
 
@@ -70,18 +70,21 @@ def build(jobs: int | None = None) -> str:
 
 ASAN_DIR = os.path.join(BUILD, "asan")
 HOST_CHECK = os.path.join(ASAN_DIR, "host_check")
+BLOCK_CHECK = os.path.join(ASAN_DIR, "block_check")
 HOST_CHECK_SRC = os.path.join(ROOT, "tests", "sanitize", "host_check.cpp")
-HOST_SRCS = sorted(glob.glob(os.path.join(CSRC, "*.cpp")))  # the C-ABI runtime
+BLOCK_CHECK_SRC = os.path.join(ROOT, "tests", "sanitize", "block_check.cpp")
+HOST_SRCS = sorted(glob.glob(os.path.join(CSRC, "*.cpp")))  # the library's host logic
 # sanitizers on the host side only: the device code is built as usual
 SANITIZE = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
             "-Xarch_host", "-fno-sanitize-recover=undefined", "-Xarch_host", "-fno-omit-frame-pointer"]
 
 
 def build_host_check() -> str:
-    """The host-code check binary: the C-ABI runtime (runtime.cpp and
-    block_api.cpp, the library's host logic) built with AddressSanitizer and
-    UndefinedBehaviorSanitizer on its host side, linked with the kernel
-    objects of the regular build and tests/sanitize/host_check.cpp."""
+    """The host-code check binaries: the host sources (runtime.cpp,
+    block_api.cpp, linear_plan.cpp) built with AddressSanitizer and
+    UndefinedBehaviorSanitizer on their host side, linked with the kernel
+    objects of the regular build, whose own host code (the launches) is not
+    sanitized, and with tests/sanitize/host_check.cpp or block_check.cpp."""
     os.makedirs(ASAN_DIR, exist_ok=True)
     kernels = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
     objs = [os.path.join(BUILD, os.path.basename(k) + ".o") for k in kernels]
@@ -90,19 +93,21 @@ def build_host_check() -> str:
     flags = ["-O1", "-g", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
              "-Wno-unused-command-line-argument", "-I", os.path.join(ROOT, "include"), "-I", CSRC]
-    main_obj = os.path.join(ASAN_DIR, "host_check.o")
+    mains = {HOST_CHECK: HOST_CHECK_SRC, BLOCK_CHECK: BLOCK_CHECK_SRC}
     rt_objs = [os.path.join(ASAN_DIR, os.path.basename(h) + ".o") for h in HOST_SRCS]
     cmds = [[HIPCC] + flags + SANITIZE + ["-x", "hip", "-c", h, "-o", o] for h, o in zip(HOST_SRCS, rt_objs)]
-    for cmd in cmds + [[HIPCC] + flags + SANITIZE + ["-c", HOST_CHECK_SRC, "-o", main_obj]]:
+    cmds += [[HIPCC] + flags + SANITIZE + ["-c", src, "-o", exe + ".o"] for exe, src in mains.items()]
+    for cmd in cmds:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"sanitized host build failed:\n{r.stderr}")
-    tmp = HOST_CHECK + ".tmp"
-    r = subprocess.run([HIPCC, f"--offload-arch={ARCH}"] + SANITIZE + ["-o", tmp, main_obj] + rt_objs + objs,
-                       capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"host check link failed:\n{r.stderr}")
-    os.replace(tmp, HOST_CHECK)
+    for exe in mains:
+        tmp = exe + ".tmp"
+        r = subprocess.run([HIPCC, f"--offload-arch={ARCH}"] + SANITIZE + ["-o", tmp, exe + ".o"] + rt_objs + objs,
+                           capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"host check link failed:\n{r.stderr}")
+        os.replace(tmp, exe)
     return HOST_CHECK
 
 

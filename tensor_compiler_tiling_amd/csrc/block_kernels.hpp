@@ -1,5 +1,5 @@
 // Host-visible declarations of the transformer-block kernels: the linear
-// layer (linear.hip) and the row operators (rows.hip).  Arguments are checked
+// layer (linear.hip, its plan linear_plan.cpp) and the row operators (rows.hip).  Arguments are checked
 // by the C entry points (block_api.cpp) before they get here.
 #pragma once
 
@@ -11,6 +11,8 @@ namespace ct {
 // y = act(scale * x w^T + bias) * gate + residual (include/convtile.h).
 // Pointers and strides are in bytes: a stage of the reduction is 128 bytes of
 // a row whatever the type.
+constexpr int kStage = 128;
+
 struct LinearParams {
     const char* x;       // [M] rows of K elements, ldx bytes apart
     const char* w;       // [N] rows of K elements, ldw bytes apart
@@ -48,6 +50,12 @@ struct LinearPlan {
     int S;     // workgroups that share each of the others, with parts of its reduction
     int pack;  // copy x and w to rows of whole stages first
 };
+
+// Stages of each of the S parts of a sum over rows of kbytes (the last may have
+// fewer, none has none: S comes from the plan).
+inline int linear_part_stages(int kbytes, int S) { return ((kbytes + kStage - 1) / kStage + S - 1) / S; }
+// Bytes between rows that are copied to whole stages.
+inline int linear_pack_pitch(int kbytes) { return (kbytes + kStage - 1) / kStage * kStage; }
 
 // The form and split for a product of these sizes (kbytes: bytes of a row).
 LinearPlan linear_plan(int M, int N, int kbytes, int dtype);
