@@ -1031,8 +1031,10 @@ hipError_t launch_dt(const LinearPlan& plan, const LinearParams& p, bool aligned
             return aligned ? launch_tile<DT, 2, 2, 2, 2, 2, 2, true>(p, plan, stream)
                            : launch_tile<DT, 2, 2, 2, 2, 2, 2, false>(p, plan, stream);
         case LIN_T128:
-            return aligned ? launch_tile<DT, 2, 2, 2, 2, 1, 2, true>(p, plan, stream)
-                           : launch_tile<DT, 2, 2, 2, 2, 1, 2, false>(p, plan, stream);
+            // fp32 comes here only in the place of 256 x 256 tiles that are not aligned
+            if constexpr (DT != DT_F32)
+                if (aligned) return launch_tile<DT, 2, 2, 2, 2, 1, 2, true>(p, plan, stream);
+            return launch_tile<DT, 2, 2, 2, 2, 1, 2, false>(p, plan, stream);
         default: return launch_tile<DT, 2, 4, 4, 2, 1, 2, true>(p, plan, stream);
     }
 }
