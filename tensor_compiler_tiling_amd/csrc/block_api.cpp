@@ -94,12 +94,18 @@ int rows_call(const void* x, long long ldx, const void* residual, long long ldr,
     return e == hipSuccess ? CT_OK : hip_fail(e, norm ? "rmsnorm launch" : "quantize launch");
 }
 
-int check_product(int M, int N, int K, int dtype, bool q8) {
+// Sizes and type of a product, whose plan goes to `plan` (not for M = 0).
+int check_product(int M, int N, int K, int dtype, bool q8, LinearPlan* plan) {
     if (M < 0 || N < 1 || K < 1) return fail(CT_ERR_INVALID_ARG, "M must not be negative, N and K must be positive");
     if (q8 ? dtype != CT_E4M3 : !plain_dtype(dtype)) return fail(CT_ERR_INVALID_ARG, "unknown dtype %d", dtype);
     if (M > kMaxRows || N > kMaxRows || (long long)K * elem_bytes(dtype) > kMaxRows)
         return fail(CT_ERR_UNSUPPORTED, "M, N and the bytes of a row must be at most 2^30");
     if (((M + 63LL) / 64) * ((N + 63LL) / 64) > 0x7fffffffLL) return fail(CT_ERR_UNSUPPORTED, "too many tiles");
+    if (M == 0) return CT_OK;
+    *plan = linear_plan(M, N, K * elem_bytes(dtype), dtype);
+    // 512 threads each: fewer than 2^32 in a launch
+    const long long groups = linear_workgroups(*plan, M, N);
+    if (groups >= 1LL << 23) return fail(CT_ERR_UNSUPPORTED, "%lld tiles: more than one launch takes", groups);
     return CT_OK;
 }
 
@@ -107,7 +113,8 @@ int linear_call(const void* x, long long ldx, const float* xs, const void* w, lo
                 long long ldy, int M, int N, int K, int dtype, int out_dtype, const ct_linear_epilogue* epi,
                 void* workspace, long long workspace_bytes, void* stream) {
     const bool q8 = dtype == CT_E4M3;
-    int st = check_product(M, N, K, dtype, q8);
+    LinearPlan plan{};
+    int st = check_product(M, N, K, dtype, q8, &plan);
     if (st != CT_OK) return st;
     if (!plain_dtype(out_dtype)) return fail(CT_ERR_INVALID_ARG, "unknown out_dtype %d", out_dtype);
     const ct_linear_epilogue none{CT_ACT_NONE, nullptr, nullptr, 0, nullptr, 0};
@@ -135,9 +142,6 @@ int linear_call(const void* x, long long ldx, const float* xs, const void* w, lo
     if ((M > 1 && p.ldx > kMaxStride) || (N > 1 && p.ldw > kMaxStride))
         return fail(CT_ERR_UNSUPPORTED, "rows of x and w must be at most 8 MiB apart");
     p.kbytes = K * es;
-    const LinearPlan plan = linear_plan(M, N, p.kbytes, dtype);
-    if (linear_workgroups(plan, M, N) >= 1LL << 23)
-        return fail(CT_ERR_UNSUPPORTED, "%lld tiles: more than one launch takes", linear_workgroups(plan, M, N));
     const long long need = linear_workspace_bytes(plan, M, N, p.kbytes);
     if (need > 0) {
         if (!workspace || workspace_bytes < need)
@@ -201,11 +205,10 @@ int ct_linear_q8_fwd(const void* x, long long ldx, const float* xs, const void* 
 }
 
 long long ct_linear_workspace_bytes(int M, int N, int K, int dtype) {
-    const int st = ct::check_product(M, N, K, dtype, dtype == CT_E4M3);
+    ct::LinearPlan plan{};
+    const int st = ct::check_product(M, N, K, dtype, dtype == CT_E4M3, &plan);
     if (st != CT_OK) return st;
-    if (M == 0) return 0;
-    const int kbytes = K * (dtype == CT_F32 ? 4 : dtype == CT_E4M3 ? 1 : 2);
-    return ct::linear_workspace_bytes(ct::linear_plan(M, N, kbytes, dtype), M, N, kbytes);
+    return M == 0 ? 0 : ct::linear_workspace_bytes(plan, M, N, K * ct::elem_bytes(dtype));
 }
 
 }  // extern "C"

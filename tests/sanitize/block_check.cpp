@@ -90,6 +90,10 @@ void plan(int M, int N, int K, int dt, long long* forms) {
     }
     const int kbytes = K * es;
     const ct::LinearPlan p = ct::linear_plan(M, N, kbytes, dt);
+    if (ct::linear_workgroups(p, M, N) >= 1 << 23) {  // the product refuses: so does the question
+        CHECK(need == CT_ERR_UNSUPPORTED);
+        return;
+    }
     CHECK(need == ct::linear_workspace_bytes(p, M, N, kbytes));
     CHECK(p.form >= ct::LIN_ROW16 && p.form <= ct::LIN_T256 && p.S >= 1 && p.S <= 16);
     ++forms[p.form];

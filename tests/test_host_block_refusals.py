@@ -89,3 +89,13 @@ def test_raw_entry_points_refuse_host_tensors(call, name):
         f(**{**args, name: torch.zeros(4, 64)})
     with pytest.raises(TypeError):
         f(**{**args, name: [0.0] * 256})
+
+
+@pytest.mark.parametrize("mnk", [(1 << 30, 64, 64), (1 << 30, 512, 1), (1, 1 << 28, 64), (1 << 20, 1 << 20, 64)], ids=str)
+def test_no_workspace_is_named_for_a_product_that_is_refused(mnk):
+    M, N, K = mnk
+    for dtype in (ct.CT_F32, ct.CT_F16, ct.CT_BF16):
+        a = {**LIN, "M": M, "N": N, "K": K, "ldy": N, "dtype": dtype, "workspace": P, "workspace_bytes": 1 << 60}
+        assert ct.ct_linear_fwd(**a) == ct.CT_ERR_UNSUPPORTED
+        assert ct.ct_linear_workspace_bytes(M, N, K, dtype) == ct.CT_ERR_UNSUPPORTED
+    assert ct.ct_linear_workspace_bytes(M, N, K, ct.CT_E4M3) == ct.CT_ERR_UNSUPPORTED
