@@ -335,9 +335,10 @@ int ct_conv2d_nchw_depthwise(const void* x, const void* w, float* y,
  * Rows.  Every matrix here is a run of rows with contiguous elements; ld* is
  * the distance between rows in elements (>= the row's length, at most 8 MiB
  * where a product reads more than one row).  Pointers are aligned to their
- * element; rows that are not multiples of 16 bytes are read at full width all
- * the same, only the loads that write LDS directly need that alignment.  M =
- * 0 rows (an empty batch) is a legal call that does nothing.
+ * element; rows that are not multiples of 16 bytes, or start off them, are read
+ * at full width all the same, but the loads that write LDS directly need that
+ * alignment: products of more than 32 such rows may take up to twice as long.
+ * M = 0 rows (an empty batch) is a legal call that does nothing.
  *
  * 8-bit rows are e4m3 (OCP: largest value 448, NaN, no infinity) with one
  * fp32 scale a row: the row stands for scale * q.  From a row of values v:
@@ -378,6 +379,9 @@ int ct_rmsnorm_fwd(const void* x, long long ldx, const void* residual, long long
 int ct_quantize_rows(const void* x, long long ldx, void* q, long long ldq, float* scale,
                      int M, int D, int dtype, void* stream);
 
+/* Each in fp32 to a few units in the last place of its value, the negative
+ * tails included (relative errors grow as z^2 2^-23 with gelu and |u| 2^-21 with
+ * gelu_tanh, u its exponent); 16-bit results to 2^-17 before their rounding. */
 enum ct_activation {
     CT_ACT_NONE = 0,
     CT_ACT_RELU = 1,

@@ -366,7 +366,7 @@ __device__ __forceinline__ void load_shifted(const char* p, unsigned sh, uint4v&
 // and the next), so every load of w is used once and nothing passes through
 // LDS before the waves' sums are joined there.  AL: rows start at dwords.
 // Measured: one row, bf16, 8192 x 8192 weights (not in the caches) 28 us, 4.8
-// TB/s, where a device copy moves 5.1 to 5.2; 4096 x 4096 (in them) 7.9 us.
+// TB/s, where a device copy moves 5.1 to 5.2; 4096 x 4096 (in them) 8.1 us.
 constexpr int kRowWaves = 8;
 
 template <int DT, int MF, bool AL>

@@ -64,7 +64,8 @@ long long linear_workspace_bytes(const LinearPlan& plan, int M, int N, int kbyte
 //
 // Up to 32 rows of x, a row form where that is expected to take less, or less
 // than the 11 us that the host needs for a split product's two launches (it
-// splits no sum over workgroups and reads the weights once).  Measured on the
+// splits no sum over workgroups and reads the weights once; in a captured graph
+// the tiles would be up to 1 us ahead on some of these).  Measured on the
 // device, row form against tiles: 8 rows, bf16, 4096 x 4096 8.9 and 10.1, 1024 x
 // 4096 8.3 and 7.4, 1024 x 8192 14.0 and 9.9, 256 x 16384 24.9 and 8.7; 24 rows, 1024
 // x 1024 4.8 and 5.8, 4096 x 4096 12.3 and 11.8, 16384 x 1024 12.2 and 9.2; fp32 4096
@@ -109,7 +110,9 @@ LinearPlan linear_plan(int M, int N, int kbytes, int dtype) {
     // 1472 x 169 x 11597 69, 99 copied);
     // copying both operands to whole stages costs their bytes twice at about
     // 4.5 TB/s and a launch (4096 x 4096 x 4095 fp16 204 us through registers,
-    // 150 copied; e4m3 133 and 74).
+    // 150 copied; e4m3 133 and 74).  Rows of whole chunks that start off 16 bytes go
+    // through registers too (4096 x 4096 x 4096 fp16 240 us, 116 aligned), never
+    // copied: the plan, and with it the workspace, goes by the sizes alone.
     if (kbytes % 16) best.pack = 2.0 * (M + (double)N) * kbytes / 4.5e6 + 2.5 < (f32 ? 0.17 : 0.7) * best_us;
     return best;
 }
