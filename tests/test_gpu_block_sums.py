@@ -51,7 +51,7 @@ def test_few_rows_of_8_bits_have_fp32_sums(mnk):
         assert torch.equal(z, y.to(out_dtype)), (mnk, out_dtype, int((z != y.to(out_dtype)).sum()))
 
 
-@pytest.mark.parametrize("mnk", [(70, 200, 512), (130, 520, 4096), (2100, 2050, 512), (4200, 4100, 512)], ids=str)
+@pytest.mark.parametrize("mnk", [(70, 200, 512), (130, 520, 4096), (2100, 2050, 512), (4200, 4100, 512), (4090, 4000, 1024)], ids=str)
 def test_what_the_8_bit_instruction_cuts(mnk):
     """16-bit results of more rows come from the 8-bit matrix instruction, which
     cuts what lies 2^-13 below the largest of 8 neighbouring products.  The size
