@@ -72,7 +72,7 @@ enum ct_dtype {
     CT_F32 = 0,
     CT_F16 = 1,
     CT_BF16 = 2,
-    CT_E4M3 = 3  /* OCP 8-bit float; transformer-block rows only (below)      */
+    CT_E4M3 = 3  /* OCP 8-bit float; transformer blocks only (below)          */
 };
 enum ct_epilogue { CT_EPI_NONE = 0, CT_EPI_BIAS = 1, CT_EPI_EXP_BIAS_RSQRT = 2 };
 enum ct_bcast_op { CT_BC_EXP = 0 };
@@ -448,6 +448,130 @@ int ct_linear_q8_fwd(const void* x, long long ldx, const float* xs,
  * CT_E4M3 for ct_linear_q8_fwd); < 0 (a status) for sizes or a dtype the
  * product refuses.  Host only. */
 long long ct_linear_workspace_bytes(int M, int N, int K, int dtype);
+
+/* ---- key-value cache and attention -----------------------------------
+ * What a transformer block does between its projections when serving: new
+ * tokens' keys and values go into a cache, and the tokens attend over it.
+ *
+ * The cache is a pool of pages, each with `page` places for rows of `dim`
+ * elements in every head.  A sequence's place i lies at place i % page of the page
+ * that its row of `table` names for i / page; without a table, sequence b has
+ * page b and no other.  Any order of the axes will do: ld_* are the distances,
+ * in elements, between pages, heads and places (the same in k and v), lds_* those
+ * of the scales.  Rows are contiguous, 16-byte aligned, of a whole multiple
+ * of 16 elements up to 256.  CT_F16 and CT_BF16 caches hold values; CT_E4M3 ones
+ * codes with a scale a place and head, made from a row of values v by
+ *   a = max(largest finite |v|, 2^-100)
+ *   s = the least power of two with a <= 448 s,  code = rne_e4m3(v / s)
+ * and standing for s * code.  What is not finite becomes the NaN code. */
+typedef struct ct_kv_cache {
+    void* k;         /* [pages][heads][page][dim] of dtype */
+    void* v;
+    float* k_scale;  /* [pages][heads][page], CT_E4M3 only (NULL otherwise); */
+    float* v_scale;  /* attention takes their sign and fraction for 0        */
+    int dtype, pages, heads, page, dim;
+    long long ld_page, ld_head, ld_token;
+    long long lds_page, lds_head, lds_token;
+} ct_kv_cache;
+
+/* The tokens of a call: rows starts[b] to starts[b + 1] - 1 are the new tokens of
+ * sequence b; without starts every sequence has tokens / sequences of them.
+ * lens[b] counts the places in use WITH the new tokens, which are the last:
+ * token i of n has place lens[b] - n + i.  lens, starts and table are read on the
+ * device when the call runs, so a captured graph follows them.  Tokens before
+ * starts[0] and from starts[sequences] on belong to nobody: their rows are
+ * not used and not written.  Contents that do not fit are the caller's fault, but
+ * lead nowhere else: lens are taken as 0 to 2^30, starts as 0 to tokens (an end
+ * before its start as no tokens; what rows of two sequences become is not said),
+ * places past the table's columns as not there; what a page number outside of
+ * the pool does is said at each call. */
+typedef struct ct_kv_batch {
+    int tokens, sequences;
+    const int* lens;    /* [sequences] */
+    const int* starts;  /* [sequences + 1], or NULL */
+    const int* table;   /* [sequences][width], rows ldt apart, or NULL */
+    long long ldt;
+    int width;
+} ct_kv_batch;
+
+/* New tokens' k and v, [tokens][heads][dim] of `dtype` (CT_F32, CT_F16 or
+ * CT_BF16), into their places: rounded to a 16-bit cache's type, or to e4m3 as
+ * above.  *_token and *_head are distances in elements (slices of a fused
+ * projection's rows will do).  A token whose place or page does not exist is
+ * left out.  Two tokens of a call must not have one place: no page may be two
+ * sequences' where they write.  Neither may overlap the cache.
+ * tokens = 0 is a legal call that does nothing.  None of the calls of this section
+ * allocates, synchronises or needs the device to have been set up: all may be
+ * captured as a stream's first work.
+ * Errors: CT_ERR_INVALID_ARG for NULL or misaligned pointers, counts that are not
+ * positive, strides that are negative or let rows of the cache (or of k and v, when
+ * they are written) overlap, an unknown dtype, scales missing (or given without
+ * CT_E4M3), more sequences than pages without a table, or tokens that the
+ * sequences do not divide without starts; CT_ERR_UNSUPPORTED for a dim that is no
+ * multiple of 16 or above 256, 2^26 rows (tokens x heads) or more, or more than
+ * 2^30 places a sequence, 2^24 sequences or 2^16 heads; CT_ERR_HIP on a launch failure.
+ * Asynchronous on `stream`. */
+int ct_kv_write(const ct_kv_cache* cache, const ct_kv_batch* batch, const void* k,
+                long long k_token, long long k_head, const void* v, long long v_token,
+                long long v_head, int dtype, void* stream);
+
+/* The last tokens of every sequence back out of the cache, as values rounded
+ * to `dtype`: what ct_kv_write would take.  A token whose place or page does not
+ * exist gives zeros.  Errors as for ct_kv_write. */
+int ct_kv_read(const ct_kv_cache* cache, const ct_kv_batch* batch, void* k, long long k_token,
+               long long k_head, void* v, long long v_token, long long v_head, int dtype,
+               void* stream);
+
+/* Which places a token sees.  Without a tree, those up to its own, of which with
+ * a window only the last `window` (its own among them) and the first `sinks`.
+ * With a tree the new tokens of a sequence are drafted nodes: node i sees the
+ * context (the places before the new tokens) and node j if bit j % 64 of word
+ * j / 64 of its row is set, its own bit among them if it is to see itself; bits past
+ * the sequence's nodes and nodes past the words count as not set.  For window
+ * and sinks, the nodes that i sees are taken in order to lie behind the context, one
+ * place each, and i's place is the last of them. */
+typedef struct ct_kv_mask {
+    int window;             /* 0: none */
+    int sinks;              /* with a window only */
+    const long long* tree;  /* [tokens][words], or NULL */
+    int words;              /* 0 without a tree */
+} ct_kv_mask;
+
+/* Attention of the new tokens over the cache, which holds them already:
+ *   y = sum_j exp(scale q . k_j) v_j / sum_j exp(scale q . k_j)
+ * over the places j that a token sees; zeros where it sees none.  q and y are
+ * [tokens][heads][dim] of `dtype` (CT_F16 or CT_BF16, that of a 16-bit cache);
+ * `heads` is a multiple of the cache's, whose head h the heads h * heads / cache
+ * heads and following share.  mask may be NULL (causal).  max_len: the longest
+ * of lens if the caller knows (0 otherwise); it only guides how the work is divided.
+ * Sums, maximum and weights are fp32; the weights are rounded to `dtype` for the
+ * product with v.  With CT_F16 and 8-bit rows, these must stay within the
+ * range of fp16.  What lies in places that a token does not see has no part in its
+ * result, whatever it is; NaN and infinities that it sees do.  A page number
+ * outside of the pool is read as page 0.
+ * Few tokens have their keys split over workgroups, whose sums are joined in
+ * order: a result depends on the sizes and the batch's contents and repeats
+ * bit for bit.  That needs `workspace`, of at least
+ * ct_kv_attention_workspace_bytes bytes for the same sizes (often 0; then it may
+ * be NULL), 16-byte aligned and free again when the call's work on the stream is
+ * done: calls that may overlap, and graphs that may be replayed at the same time,
+ * need one each.  y must not overlap q or the cache.
+ * Errors: those of ct_kv_write, and CT_ERR_INVALID_ARG for a scale that is not
+ * positive and finite, heads that are no multiple of the cache's, a negative
+ * window, sinks without a window, words without a tree (or the reverse), another
+ * type than that of a 16-bit cache, or a workspace that is too small;
+ * CT_ERR_UNSUPPORTED for 2^26 rows of q (tokens x heads) or more, or more than
+ * 2^23 workgroups.  Asynchronous on `stream`. */
+int ct_kv_attention_fwd(const ct_kv_cache* cache, const ct_kv_batch* batch, const ct_kv_mask* mask,
+                        const void* q, long long q_token, long long q_head, void* y,
+                        long long y_token, long long y_head, int heads, int dtype, float scale,
+                        long long max_len, void* workspace, long long workspace_bytes,
+                        void* stream);
+
+/* Bytes of workspace that a call of these sizes needs (window 0: none); < 0 (a
+ * status) for sizes that it refuses.  Host only. */
+long long ct_kv_attention_workspace_bytes(int tokens, int sequences, int heads, int kv_heads,
+                                          int dim, long long max_len, int window, int sinks);
 
 /* ---- tile-config search ----------------------------------------------
  * The space of a shape follows the TVM tutorial's template (Step 1): ordered

@@ -7,7 +7,7 @@ linked into tensor_compiler_tiling_amd/libconvtile.so.
 
 build_host_check() also compiles the host sources (csrc/*.cpp) with
 AddressSanitizer and UndefinedBehaviorSanitizer on their host side and links
-them with tests/sanitize/host_check.cpp and block_check.cpp into
+them with the programs of tests/sanitize/ into
 _build/asan/, CPU-only checks of the library's host code.
 """
 from __future__ import annotations
@@ -71,8 +71,10 @@ def build(jobs: int | None = None) -> str:
 ASAN_DIR = os.path.join(BUILD, "asan")
 HOST_CHECK = os.path.join(ASAN_DIR, "host_check")
 BLOCK_CHECK = os.path.join(ASAN_DIR, "block_check")
+ATTENTION_CHECK = os.path.join(ASAN_DIR, "attention_check")
 HOST_CHECK_SRC = os.path.join(ROOT, "tests", "sanitize", "host_check.cpp")
 BLOCK_CHECK_SRC = os.path.join(ROOT, "tests", "sanitize", "block_check.cpp")
+ATTENTION_CHECK_SRC = os.path.join(ROOT, "tests", "sanitize", "attention_check.cpp")
 HOST_SRCS = sorted(glob.glob(os.path.join(CSRC, "*.cpp")))  # the library's host logic
 # sanitizers on the host side only: the device code is built as usual
 SANITIZE = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
@@ -81,10 +83,10 @@ SANITIZE = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=unde
 
 def build_host_check() -> str:
     """The host-code check binaries: the host sources (runtime.cpp,
-    block_api.cpp, linear_plan.cpp) built with AddressSanitizer and
+    block_api.cpp, linear_plan.cpp, attention_api.cpp, attention_plan.cpp) built with AddressSanitizer and
     UndefinedBehaviorSanitizer on their host side, linked with the kernel
     objects of the regular build, whose own host code (the launches) is not
-    sanitized, and with tests/sanitize/host_check.cpp or block_check.cpp."""
+    sanitized, and each with a program of tests/sanitize/."""
     os.makedirs(ASAN_DIR, exist_ok=True)
     kernels = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
     objs = [os.path.join(BUILD, os.path.basename(k) + ".o") for k in kernels]
@@ -93,7 +95,7 @@ def build_host_check() -> str:
     flags = ["-O1", "-g", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
              "-Wno-unused-command-line-argument", "-I", os.path.join(ROOT, "include"), "-I", CSRC]
-    mains = {HOST_CHECK: HOST_CHECK_SRC, BLOCK_CHECK: BLOCK_CHECK_SRC}
+    mains = {HOST_CHECK: HOST_CHECK_SRC, BLOCK_CHECK: BLOCK_CHECK_SRC, ATTENTION_CHECK: ATTENTION_CHECK_SRC}
     rt_objs = [os.path.join(ASAN_DIR, os.path.basename(h) + ".o") for h in HOST_SRCS]
     cmds = [[HIPCC] + flags + SANITIZE + ["-x", "hip", "-c", h, "-o", o] for h, o in zip(HOST_SRCS, rt_objs)]
     cmds += [[HIPCC] + flags + SANITIZE + ["-c", src, "-o", exe + ".o"] for exe, src in mains.items()]

@@ -62,6 +62,25 @@ class ct_linear_epilogue(ctypes.Structure):
                 ("ldg", ctypes.c_longlong), ("residual", ctypes.c_void_p), ("ldr", ctypes.c_longlong)]
 
 
+class ct_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("dtype", ctypes.c_int), ("pages", ctypes.c_int),
+                ("heads", ctypes.c_int), ("page", ctypes.c_int), ("dim", ctypes.c_int),
+                ("ld_page", ctypes.c_longlong), ("ld_head", ctypes.c_longlong), ("ld_token", ctypes.c_longlong),
+                ("lds_page", ctypes.c_longlong), ("lds_head", ctypes.c_longlong), ("lds_token", ctypes.c_longlong)]
+
+
+class ct_kv_batch(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int), ("sequences", ctypes.c_int), ("lens", ctypes.c_void_p),
+                ("starts", ctypes.c_void_p), ("table", ctypes.c_void_p), ("ldt", ctypes.c_longlong),
+                ("width", ctypes.c_int)]
+
+
+class ct_kv_mask(ctypes.Structure):
+    _fields_ = [("window", ctypes.c_int), ("sinks", ctypes.c_int), ("tree", ctypes.c_void_p),
+                ("words", ctypes.c_int)]
+
+
 class ct_tvm_config(ctypes.Structure):
     _fields_ = [("tile_f", ctypes.c_int * 4), ("tile_y", ctypes.c_int * 4), ("tile_x", ctypes.c_int * 4),
                 ("tile_rc", ctypes.c_int * 3), ("tile_ry", ctypes.c_int * 3), ("tile_rx", ctypes.c_int * 3),
@@ -149,6 +168,10 @@ _SIGS = {
     "ct_linear_fwd": (_I, [_P, _LL, _P, _LL, _P, _LL] + [_I] * 5 + [_P, _P, _LL, _P]),
     "ct_linear_q8_fwd": (_I, [_P, _LL, _P, _P, _LL, _P, _P, _LL] + [_I] * 4 + [_P, _P, _LL, _P]),
     "ct_linear_workspace_bytes": (_LL, [_I] * 4),
+    "ct_kv_write": (_I, [_P, _P, _P, _LL, _LL, _P, _LL, _LL, _I, _P]),
+    "ct_kv_read": (_I, [_P, _P, _P, _LL, _LL, _P, _LL, _LL, _I, _P]),
+    "ct_kv_attention_fwd": (_I, [_P, _P, _P, _P, _LL, _LL, _P, _LL, _LL, _I, _I, _F, _LL, _P, _LL, _P]),
+    "ct_kv_attention_workspace_bytes": (_LL, [_I] * 5 + [_LL, _I, _I]),
     "ct_variant_count": (_I, []),
     "ct_variant_info": (_I, [_I, ctypes.POINTER(ct_variant_desc)]),
     "ct_split_count": (_LL, [_LL, _I]),
@@ -391,6 +414,35 @@ def ct_linear_q8_fwd(x, ldx, xs, w, ldw, ws, y, ldy, M, N, K, out_dtype, epi: Op
     return _load().ct_linear_q8_fwd(_row_ptr(x), ldx, _ptr(xs), _row_ptr(w), ldw, _ptr(ws), _row_ptr(y), ldy, M, N,
                                     K, out_dtype, ctypes.addressof(epi) if epi is not None else None,
                                     _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+# The structs of these are kept alive by the caller for the call; the counts in
+# them are held to 32 bits by KVCache and the helpers.
+def _struct(t):
+    return ctypes.addressof(t) if isinstance(t, ctypes.Structure) else t
+
+
+def ct_kv_write(cache, batch, k, k_token, k_head, v, v_token, v_head, dtype, stream=None) -> int:
+    return _load().ct_kv_write(_struct(cache), _struct(batch), _row_ptr(k), k_token, k_head, _row_ptr(v), v_token,
+                               v_head, dtype, _stream(stream))
+
+
+def ct_kv_read(cache, batch, k, k_token, k_head, v, v_token, v_head, dtype, stream=None) -> int:
+    return _load().ct_kv_read(_struct(cache), _struct(batch), _row_ptr(k), k_token, k_head, _row_ptr(v), v_token,
+                              v_head, dtype, _stream(stream))
+
+
+def ct_kv_attention_fwd(cache, batch, mask, q, q_token, q_head, y, y_token, y_head, heads, dtype, scale, max_len=0,
+                        workspace=None, workspace_bytes=0, stream=None) -> int:
+    _counts(heads=heads)
+    return _load().ct_kv_attention_fwd(_struct(cache), _struct(batch), _struct(mask), _row_ptr(q), q_token, q_head,
+                                       _row_ptr(y), y_token, y_head, heads, dtype, scale, max_len, _ptr(workspace),
+                                       workspace_bytes, _stream(stream))
+
+
+def ct_kv_attention_workspace_bytes(tokens, sequences, heads, kv_heads, dim, max_len=0, window=0, sinks=0) -> int:
+    _counts(tokens=tokens, sequences=sequences, heads=heads, kv_heads=kv_heads, dim=dim, window=window, sinks=sinks)
+    return _load().ct_kv_attention_workspace_bytes(tokens, sequences, heads, kv_heads, dim, max_len, window, sinks)
 
 
 def ct_linear_workspace_bytes(M, N, K, dtype) -> int:
@@ -677,7 +729,7 @@ class _TorchSide:
         import torch
         self.empty, self.Tensor = torch.empty_strided, torch.Tensor  # the form that parses fastest
         self.f32, self.bf16, self.e4m3 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
-        self.uint8 = torch.uint8
+        self.uint8, self.i32, self.i64 = torch.uint8, torch.int32, torch.int64
         self.codes = {torch.float32: CT_F32, torch.float16: CT_F16, torch.bfloat16: CT_BF16}
         self.current_device = torch.cuda.current_device
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -932,6 +984,230 @@ def linear_q8(xq, xs, wq, ws, bias=None, act: str = "none", gate=None, residual=
     if xs is None or ws is None:
         raise ValueError("8-bit rows have scales")
     return _product(xq, xs, wq, ws, bias, act, gate, residual, out_dtype, out, stream)
+
+
+# ---- key-value cache and attention: a transformer block between its projections
+class KVCache:
+    """A pool of pages for keys and values, k and v [pages, heads, page, dim].
+
+    float16 and bfloat16 tensors hold values, torch.float8_e4m3fn ones codes
+    with fp32 scales k_scale and v_scale [pages, heads, page] (powers of two:
+    a row stands for scale * code).  Any order of the axes in memory will do
+    (views of [pages, page, heads, dim], say), the same for k and v; rows are
+    contiguous, 16-byte aligned, dim a multiple of 16 up to 256.  The tensors are
+    the caller's: their contents may be copied, moved or cleared between calls."""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "index", "device", "dtype", "pages", "heads", "page", "dim", "_c", "_at")
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        T = _side()
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride():
+            raise ValueError("k and v must be [pages, heads, page, dim] of one shape, type and layout")
+        q8 = k.dtype is T.e4m3
+        if not q8 and (k.dtype is T.f32 or k.dtype not in T.codes):
+            raise ValueError(f"a cache of {k.dtype}: float16, bfloat16 or float8_e4m3fn")
+        if (k_scale is None) is q8 or (v_scale is None) is q8:
+            raise ValueError("8-bit rows have scales, and others have none")
+        self.index = k.get_device()
+        if self.index < 0 or v.get_device() != self.index:
+            raise ValueError("k and v must be GPU tensors on one device")
+        if any(n >> 31 for n in k.shape):
+            raise ValueError(f"{list(k.shape)} does not fit 32 bits")
+        if k.shape[3] > 1 and k.stride(3) != 1:
+            raise ValueError("the elements of a row must be contiguous")
+        st = (0, 0, 0)
+        if q8:
+            for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+                if s.get_device() != self.index or s.dtype is not T.f32 or s.shape != k.shape[:3]:
+                    raise ValueError(f"{name} must be fp32 {list(k.shape[:3])} on the device of k")
+            st = k_scale.stride()
+            if v_scale.stride() != st:
+                raise ValueError("k_scale and v_scale must have one layout")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device, self.dtype = k.device, k.dtype
+        self.pages, self.heads, self.page, self.dim = k.shape
+        self._c = ct_kv_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if q8 else None,
+                              v_scale.data_ptr() if q8 else None, CT_E4M3 if q8 else T.codes[k.dtype], self.pages,
+                              self.heads, self.page, self.dim, *k.stride()[:3], *st)
+        self._at = ctypes.addressof(self._c)
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, page: int, dim: int, dtype=None, device="cuda"):
+        """A cache of `pages` pages, uninitialised (bfloat16 by default)."""
+        import torch
+        dtype = dtype or torch.bfloat16
+        k, v = (torch.empty((pages, heads, page, dim), dtype=dtype, device=device) for _ in range(2))
+        if dtype != torch.float8_e4m3fn:
+            return cls(k, v)
+        return cls(k, v, *(torch.empty((pages, heads, page), dtype=torch.float32, device=device) for _ in range(2)))
+
+
+def _integers(name: str, t, index: int, n: int) -> int:
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be a GPU tensor on the device of the cache")
+    if t.dtype is not _side().i32 or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be {n} contiguous int32 values")
+    return t.data_ptr()
+
+
+def _batch(cache: KVCache, tokens: int, lens, starts, table) -> ct_kv_batch:
+    index = cache.index
+    if lens.dim() != 1:
+        raise ValueError("lens must have one dimension")
+    sequences = lens.shape[0]
+    if (tokens | sequences) >> 31:
+        raise ValueError(f"{tokens} tokens of {sequences} sequences do not fit 32 bits")
+    sp = tp = None
+    ldt = width = 0
+    if starts is not None:
+        sp = _integers("starts", starts, index, sequences + 1)
+    if table is not None:
+        if table.get_device() != index:
+            raise ValueError("table must be a GPU tensor on the device of the cache")
+        if table.dtype is not _side().i32 or table.dim() != 2 or table.shape[0] != sequences:
+            raise ValueError(f"table must be int32 [{sequences}, columns]")
+        width = table.shape[1]
+        ldt, step = table.stride()
+        if width >> 31 or (width > 1 and step != 1):
+            raise ValueError("the elements of a table's row must be contiguous, fewer than 2^31")
+        tp = table.data_ptr()
+    return ct_kv_batch(tokens, sequences, _integers("lens", lens, index, sequences), sp, tp, ldt, width)
+
+
+def _heads(name: str, t, index: int, dtype, shape):
+    """Check [tokens, heads, dim] rows; the distances between tokens and heads."""
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be a GPU tensor on the device of the cache")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    token, head, step = t.stride()
+    if step != 1 and shape[2] > 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return token, head
+
+
+def kv_write(cache: KVCache, k, v, lens, table=None, starts=None, stream=None) -> None:
+    """New tokens' k and v [tokens, heads, dim] into the cache (fp32, fp16 or
+    bf16; slices of a fused projection's rows will do).
+
+    lens int32 [sequences] counts each sequence's places in use with the new
+    tokens, which are the last; starts int32 [sequences + 1] says which rows are
+    whose (None: equally many each); table int32 [sequences, columns] names the
+    pages (None: sequence b has page b).  All three are read on the device."""
+    T = _side()
+    index = cache.index
+    if k.dim() != 3:
+        raise ValueError("k must be [tokens, heads, dim]")
+    if stream is not None or index != T.current_device():
+        with _elsewhere(cache.device, stream):
+            return kv_write(cache, k, v, lens, table, starts)
+    shape = (k.shape[0], cache.heads, cache.dim)
+    kt, kh = _heads("k", k, index, k.dtype, shape)
+    vt, vh = _heads("v", v, index, k.dtype, shape)
+    b = _batch(cache, shape[0], lens, starts, table)
+    st = _load().ct_kv_write(cache._at, ctypes.addressof(b), k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, _code(k.dtype),
+                             T.stream(index))
+    if st:
+        check(st, "kv_write")
+
+
+def kv_read(cache: KVCache, tokens: int, lens, table=None, starts=None, dtype=None, k=None, v=None, stream=None):
+    """The last tokens of every sequence out of the cache: (k, v), each
+    [tokens, heads, dim] of dtype (the cache's own, or bf16 from 8 bits, by default).
+    tokens counts them all; lens, table and starts as for kv_write.  Rows of
+    tokens that belong to no sequence are left as they are (k and v may name
+    the tensors to write)."""
+    T = _side()
+    index = cache.index
+    if stream is not None or index != T.current_device():
+        with _elsewhere(cache.device, stream):
+            return kv_read(cache, tokens, lens, table, starts, dtype, k, v)
+    if tokens < 0:
+        raise ValueError("tokens must not be negative")
+    if dtype is None:
+        dtype = k.dtype if k is not None else v.dtype if v is not None else T.bf16 if cache.dtype is T.e4m3 else cache.dtype
+    shape = (tokens, cache.heads, cache.dim)
+    b = _batch(cache, tokens, lens, starts, table)
+    step = (cache.heads * cache.dim, cache.dim, 1)
+    if k is None:
+        k = T.empty(shape, step, dtype=dtype, device=cache.device)
+    if v is None:
+        v = T.empty(shape, step, dtype=dtype, device=cache.device)
+    kt, kh = _heads("k", k, index, dtype, shape)
+    vt, vh = _heads("v", v, index, dtype, shape)
+    st = _load().ct_kv_read(cache._at, ctypes.addressof(b), k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, _code(dtype),
+                            T.stream(index))
+    if st:
+        check(st, "kv_read")
+    return k, v
+
+
+@functools.lru_cache(maxsize=4096)
+def _attention_bytes(*sizes) -> int:
+    return max(0, _load().ct_kv_attention_workspace_bytes(*sizes))
+
+
+def kv_attention(q, cache: KVCache, lens, table=None, starts=None, max_len=None, window: int = 0, sinks: int = 0,
+                 tree=None, scale=None, out=None, stream=None):
+    """Attention of new tokens q [tokens, heads, dim] (fp16 or bf16) over the
+    cache, which holds their keys and values already: y like q.
+
+    heads is a multiple of the cache's, whose heads groups of neighbours share.
+    lens, table and starts as for kv_write.  Each token sees the places up to its
+    own; with a window only the last `window` of them and the first `sinks`.
+    With a tree, int64 [tokens] or [tokens, words], the new tokens are drafted
+    nodes: node i sees the context before them and node j if bit j of its row is
+    set, its own included.  max_len, the longest of lens where the program
+    knows, guides how the work is divided (the table's reach by default); scale is
+    dim ** -0.5 by default.  A token that sees nothing gives zeros."""
+    T = _side()
+    index = cache.index
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, heads, dim]")
+    if stream is not None or index != T.current_device():
+        with _elsewhere(cache.device, stream):
+            return kv_attention(q, cache, lens, table, starts, max_len, window, sinks, tree, scale, out)
+    shape = q.shape
+    tokens, heads, dim = shape
+    if dim != cache.dim:
+        raise ValueError(f"q has rows of {dim} and the cache of {cache.dim}")
+    if heads >> 31:
+        raise ValueError(f"{heads} heads do not fit 32 bits")
+    dtype = q.dtype
+    qt, qh = _heads("q", q, index, dtype, shape)
+    b = _batch(cache, tokens, lens, starts, table)
+    words, tp = 0, None
+    if tree is not None:
+        words = 1 if tree.dim() == 1 else tree.shape[-1]
+        if tree.get_device() != index:
+            raise ValueError("tree must be a GPU tensor on the device of the cache")
+        if tree.dtype is not T.i64 or tree.dim() > 2 or tree.shape[0] != tokens or not tree.is_contiguous() or words >> 31:
+            raise ValueError(f"tree must be contiguous int64 [{tokens}] or [{tokens}, words]")
+        tp = tree.data_ptr()
+    if not (0 <= window < 1 << 31 and 0 <= sinks < 1 << 31):
+        raise ValueError("window and sinks must be counts of 31 bits")
+    mask = None
+    if window or sinks or tp is not None:
+        keep = ct_kv_mask(window, sinks, tp, words)
+        mask = ctypes.addressof(keep)
+    if out is None:
+        out = T.empty(shape, (heads * dim, dim, 1), dtype=dtype, device=cache.device)
+    yt, yh = _heads("out", out, index, dtype, shape)
+    reach = (b.width if table is not None else 1) * cache.page
+    longest = reach if max_len is None else max(1, min(max_len, reach))
+    need = _attention_bytes(tokens, b.sequences, heads, cache.heads, dim, longest, window, sinks)
+    sp = None
+    if need:
+        space = T.empty((need,), (1,), dtype=T.uint8, device=cache.device)
+        sp = space.data_ptr()
+    st = _load().ct_kv_attention_fwd(cache._at, ctypes.addressof(b), mask, q.data_ptr(), qt, qh, out.data_ptr(), yt, yh,
+                                     heads, _code(dtype), dim ** -0.5 if scale is None else scale, longest, sp, need,
+                                     T.stream(index))
+    if st:
+        check(st, "kv_attention")
+    return out
 
 
 def broadcast(var, N: int, H: int, W: int, out_dtype=None, mode: int = CT_BC_AUTO, out=None,

@@ -1,0 +1,863 @@
+// Attention of new tokens over the key-value cache.
+//
+//   z_j = scale * q . k_j,  y = sum_j exp(z_j) v_j / sum_j exp(z_j)
+//
+// over the places j that the token sees.  One pass over the keys with the
+// running maximum m of z and the running sum: what has been summed is scaled
+// by exp(m_old - m_new) where m grows.  All of it in units of log2, with exp2.
+//
+// The heads of a group share their keys, so the rows of a product are (token,
+// head of the group) pairs, token by token, and a tile of rows reads a page
+// once for all of them.  Both products are computed transposed:
+//   Z^T [keys x rows] = K Q^T,   Y^T [dim x rows] = V^T P^T
+// An instruction's result then has one row of q a lane, whose maximum, sum and
+// scaling are the lane's own, and holds neighbouring keys in a lane's
+// registers, in the order in which the second product takes them as its right
+// operand: the weights P never leave their registers.  The left operand of the
+// second product, V^T, comes from LDS by the transposing read.
+//
+// Roundings: products of 16-bit values summed in fp32; maximum, weights and sums
+// fp32; P goes into the second product rounded to the type of q (by up to 2^-8 or 2^-11
+// of a weight, at random, as the result's own rounding), the sum of the weights
+// is made from the unrounded ones.  8-bit rows widen to 16 bits with their
+// scale, exactly in bf16.  For fp16, whose range is short, they widen to half
+// their value (448 * 2^8 would pass 65504; what falls below 2^-24 so is less than
+// fp16's own smallest step), and P is held times 2^7: with m lagging by up to
+// 2^8, below, its range is 2^-31 to 2^15 of the largest weight.
+#include "kv_device.hpp"
+
+#include <type_traits>
+
+namespace ct {
+
+namespace {
+
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+typedef _Float16 halfx8 __attribute__((ext_vector_type(8)));
+typedef _Float16 halfx2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef short shortx4 __attribute__((ext_vector_type(4)));
+typedef unsigned int uint2v __attribute__((ext_vector_type(2)));
+
+enum { DT_E4M3 = 3 };
+
+constexpr float kLag = 8.0f;  // log2 by which weights may pass 1 before what is summed is scaled
+
+// log2 of what P is held times
+template <int DT> constexpr float p_shift() { return DT == DT_F16 ? 7.0f : 0.0f; }
+
+template <int DT>
+__device__ __forceinline__ floatx16 mma32(uint4v a, uint4v b, floatx16 c) {
+    if constexpr (DT == DT_F16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(halfx8, a), __builtin_bit_cast(halfx8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+template <int DT>
+__device__ __forceinline__ floatx4 mma16(uint4v a, uint4v b, floatx4 c) {
+    if constexpr (DT == DT_F16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(halfx8, a), __builtin_bit_cast(halfx8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+template <int DT>
+__device__ __forceinline__ unsigned pack2(float a, float b) {
+    if constexpr (DT == DT_F16)
+        return __builtin_bit_cast(unsigned, halfx2{(_Float16)a, (_Float16)b});
+    else
+        return __builtin_bit_cast(unsigned, bf16x2{(__bf16)a, (__bf16)b});
+}
+
+// Four 8-bit codes times a power of two, as two dwords of the 16-bit type.
+template <int DT>
+__device__ __forceinline__ uint2v widen4(unsigned codes, float scale) {
+    if constexpr (DT == DT_F16)
+        return {__builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes, scale, false)),
+                __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes, scale, true))};
+    else
+        return {__builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, false)),
+                __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, true))};
+}
+
+// 8 values of a 16-byte piece of 16 codes.
+template <int DT>
+__device__ __forceinline__ uint4v widen8(uint4v piece, int half, float scale) {
+    const uint2v a = widen4<DT>(piece[2 * half], scale), b = widen4<DT>(piece[2 * half + 1], scale);
+    return uint4v{a[0], a[1], b[0], b[1]};
+}
+
+// Half the scale for fp16 (above); the other half is in the score's factor
+// and in the last step.
+template <int DT, bool Q8>
+__device__ __forceinline__ float used_scale(float s) { return DT == DT_F16 ? 0.5f * s : s; }
+
+// Four keys of a column: lane i of 16 names row i / 4 of 4, columns 4 (i % 4) to
+// + 3 of 16, and gets column i.
+__device__ __forceinline__ uint2v read_transposed(const uint16_t* p) {
+    typedef __attribute__((address_space(3))) shortx4 lds_short4;
+    return __builtin_bit_cast(uint2v, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)p));
+}
+
+// Keeps the compiler from moving a wave's accesses of LDS past each other; the
+// hardware runs them in order.
+__device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local"); }
+
+// A value that all lanes share, as a scalar.  What is the wave's own (its index,
+// its keys, its loop's ends) goes through this, so that the branches on it are
+// scalar too.  With conditions as masks, where registers were short, the compiler
+// (ROCm 7.2) copied values away before it had put the mask back: waves that had
+// skipped a branch lost them.
+__device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int wave_of() { return scalar((int)threadIdx.x >> 6); }
+
+__device__ __forceinline__ uint4v load16(const char* p) {
+    uint4v v;
+    __builtin_memcpy(&v, p, 16);
+    return v;
+}
+
+// Values that are not finite become 0: was there any?
+template <int DT>
+__device__ __forceinline__ bool clear_not_finite(uint4v& v) {
+    constexpr unsigned E = DT == DT_F16 ? 0x7c00u : 0x7f80u;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if ((v[i] & E) == E) v[i] &= 0xffff0000u, bad = true;
+        if (((v[i] >> 16) & E) == E) v[i] &= 0xffffu, bad = true;
+    }
+    return bad;
+}
+
+// ------------------------------------------------------------ what is seen --
+// A tile of rows of one kv head: its sequence and first row.
+struct Tile {
+    int seq, r0;       // seq < 0: none
+    int first, count;  // the sequence's new tokens
+    int len, ctx;      // keys that the pages hold, and the place of the first new token
+};
+
+// The tile-th tile of `rows` rows, counted over the sequences.  With starts,
+// every wave counts the sequences' tiles by itself, 64 at a time.
+__device__ __forceinline__ Tile find_tile(const AttendParams& p, int tile, int rows) {
+    Tile t{-1, 0, 0, 0, 0, 0};
+    if (!p.b.starts) {
+        const int per = (p.b.even * p.group + rows - 1) / rows;
+        t.seq = tile / per;
+        if (t.seq >= p.b.sequences) t.seq = -1;
+        t.r0 = (tile - t.seq * per) * rows;
+    } else {
+        const int lane = threadIdx.x & 63;
+        int before = 0;
+        for (int s0 = 0; s0 < p.b.sequences; s0 += 64) {
+            const int seq = s0 + lane;
+            int n = 0;
+            if (seq < p.b.sequences) n = (span_of(p.b, seq).count * p.group + rows - 1) / rows;
+            int upto = n;
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const int u = __shfl_up(upto, o);
+                if (lane >= o) upto += u;
+            }
+            const unsigned long long hit = __ballot(before + upto > tile);
+            if (hit) {
+                const int at = __builtin_ctzll(hit);
+                t.seq = s0 + at;
+                t.r0 = (tile - before - __shfl(upto - n, at)) * rows;
+                break;
+            }
+            before += __shfl(upto, 63);
+        }
+    }
+    if (t.seq < 0) return t;
+    t.seq = scalar(t.seq);
+    t.r0 = scalar(t.r0);
+    const Span sp = span_of(p.b, t.seq);
+    t.first = scalar(sp.first);
+    t.count = scalar(sp.count);
+    const int len = scalar(length_of(p.b, t.seq)), most = p.b.width * p.c.page;
+    t.ctx = len - t.count;
+    t.len = len < most ? len : most;
+    return t;
+}
+
+// The key tiles (of KT keys) that rows [r0, r0 + rows) of a tile can see: those
+// of the sinks, [0, sinks), then [from, from + rest).
+struct Keys {
+    int sinks, from, rest;
+    __device__ __forceinline__ int total() const { return sinks + rest; }
+    __device__ __forceinline__ int at(int i) const { return i < sinks ? i : from + i - sinks; }
+};
+
+template <int KT>
+__device__ __forceinline__ Keys keys_of(const AttendParams& p, const Tile& t, int r0, int rows) {
+    const int last = t.count * p.group - 1;
+    const int i0 = r0 / p.group, i1 = (r0 + rows - 1 < last ? r0 + rows - 1 : last) / p.group;
+    // the places of the rows' tokens: a node of a tree may lie anywhere behind the context
+    const int lowest = p.tree ? t.ctx - 1 : t.ctx + i0, highest = p.tree ? t.len - 1 : t.ctx + i1;
+    const int lo = clampi(lowest - p.window + 1, 0, t.len), hi = clampi(highest + 1, 0, t.len);
+    const int cover = (hi + KT - 1) / KT, first = ((p.sinks < lo ? p.sinks : lo) + KT - 1) / KT;
+    const int sinks = scalar(first < cover ? first : cover), from = scalar(lo / KT > sinks ? lo / KT : sinks);
+    return {sinks, from, scalar(cover > from ? cover - from : 0)};
+}
+
+// Bits [a, b) of 64.
+__device__ __forceinline__ unsigned long long bits_between(int a, int b) {
+    a = clampi(a, 0, 64);
+    b = clampi(b, 0, 64);
+    if (b <= a) return 0;
+    return (~0ull >> (64 - (b - a))) << a;
+}
+
+// What a row sees.
+struct Row {
+    int token, head;  // of the call's tokens and of q's heads; token < 0: no row
+    int pos;
+    int nodes;        // of a tree: how many drafted nodes it sees
+};
+
+__device__ __forceinline__ unsigned long long tree_word(const AttendParams& p, const Tile& t, int token, int word) {
+    const int left = t.count - word * 64;  // nodes beyond the sequence's are none
+    if (word < 0 || word >= p.words || left <= 0) return 0;
+    const unsigned long long w = (unsigned long long)p.tree[(long long)token * p.words + word];
+    return left >= 64 ? w : w & (~0ull >> (64 - left));
+}
+
+__device__ __forceinline__ Row row_of(const AttendParams& p, const Tile& t, int head0, int r) {
+    Row row{-1, 0, -1, 0};
+    if (r >= t.count * p.group) return row;
+    const int i = r / p.group;
+    row.token = t.first + i;
+    row.head = head0 + r - i * p.group;
+    row.pos = t.ctx + i;
+    if (p.tree) {
+        const int words = (t.count + 63) / 64;
+        for (int w = 0; w < words; ++w) row.nodes += __builtin_popcountll(tree_word(p, t, row.token, w));
+        row.pos = t.ctx + row.nodes - 1;
+    }
+    return row;
+}
+
+// Keys k0 to k0 + 63 that a row sees, as bits.
+__device__ __forceinline__ unsigned long long seen(const AttendParams& p, const Tile& t, const Row& row, int k0) {
+    if (row.token < 0) return 0;
+    // places before the row's own, in its window or among the sinks
+    const int end = (p.tree ? t.ctx - 1 : row.pos) + 1 - k0, all = t.len - k0;
+    unsigned long long m = bits_between(row.pos - p.window + 1 - k0, end) | bits_between(0, end < p.sinks - k0 ? end : p.sinks - k0);
+    if (p.tree && k0 + 64 > t.ctx) {
+        const int j0 = k0 - t.ctx;  // the first key as a node; negative where the tile begins in the context
+        const int word = j0 >= 0 ? j0 >> 6 : -((63 - j0) >> 6), sh = j0 - word * 64;
+        unsigned long long n = tree_word(p, t, row.token, word) >> sh;
+        if (sh) n |= tree_word(p, t, row.token, word + 1) << (64 - sh);
+        if (row.nodes > p.window) {
+            // the nodes that it sees lie at ctx, ctx + 1, ...: drop those outside of the window, but for sinks
+            int rank = 0;
+            for (int w = 0; w <= word; ++w) {
+                const unsigned long long u = tree_word(p, t, row.token, w);
+                rank += __builtin_popcountll(w < word ? u : sh ? u & (~0ull >> (64 - sh)) : 0);
+            }
+            unsigned long long left = n;
+            const int keep = p.sinks - t.ctx, drop = row.nodes - p.window;
+            for (; left && rank < drop; ++rank, left &= left - 1)
+                if (rank >= keep) n &= ~(left & -left);
+        }
+        m |= n;
+    }
+    return m & bits_between(0, all);
+}
+
+// Does every row among tokens [i0, i1] see all of keys [k0, k0 + KT)?
+template <int KT>
+__device__ __forceinline__ bool all_seen(const AttendParams& p, const Tile& t, int i0, int i1, int k0) {
+    const int lowest = p.tree ? t.ctx - 1 : t.ctx + i0, highest = p.tree ? t.ctx + t.count - 1 : t.ctx + i1;
+    if (k0 + KT > t.len || k0 + KT > lowest + 1) return false;
+    return k0 > highest - p.window || k0 + KT <= p.sinks;
+}
+
+// A weight of 0 does not clear what is not finite.  Where some row of a stage does
+// not see all of its keys, V therefore goes into the product without such values,
+// and the rows that see one get it by this: a key's value in the cache, and of
+// it what is not finite (0 for the others).
+template <int DT, bool Q8>
+struct CacheRow {
+    const char* v;
+    int dim;
+    __device__ __forceinline__ CacheRow(const AttendParams& p, const Tile& t, int head, int key) : dim(p.c.dim) {
+        const Place at = place_of(p.c, key);
+        int page = page_of(p.b, t.seq, at.index);
+        if ((unsigned)page >= (unsigned)p.c.pages) page = 0;
+        v = p.c.v + page * p.c.ld_page + at.in * p.c.ld_token + head * p.c.ld_head;
+    }
+    __device__ __forceinline__ float not_finite(int d) const {
+        if (d >= dim) return 0.0f;
+        float f;
+        if constexpr (Q8)
+            f = (v[d] & 0x7f) == 0x7f ? __builtin_nanf("") : 0.0f;
+        else
+            f = Elem<DT>::to_f32(reinterpret_cast<const typename Elem<DT>::T*>(v)[d]);
+        return __builtin_isfinite(f) ? 0.0f : f;
+    }
+};
+
+// ------------------------------------------------------------- the results --
+// Four neighbouring elements of a row's sums from d.
+template <int DT>
+__device__ __forceinline__ void put4(const AttendParams& p, const Row& row, int part, int d, float a, float b, float c,
+                                     float e, float inv) {
+    if (row.token < 0 || d >= p.c.dim) return;
+    if (p.parts > 1) {
+        const long long at = ((long long)part * p.b.tokens + row.token) * (p.c.heads * p.group) + row.head;
+        *reinterpret_cast<floatx4*>(p.part_o + at * p.c.dim + d) = floatx4{a, b, c, e};
+    } else {
+        const uint2v w = {pack2<DT>(a * inv, b * inv), pack2<DT>(c * inv, e * inv)};
+        __builtin_memcpy(p.y + row.token * p.y_token + row.head * p.y_head + d * 2, &w, 8);
+    }
+}
+
+__device__ __forceinline__ void put_weight(const AttendParams& p, const Row& row, int part, float m, float l) {
+    if (row.token < 0 || p.parts <= 1) return;
+    const long long at = ((long long)part * p.b.tokens + row.token) * (p.c.heads * p.group) + row.head;
+    p.part_ml[2 * at] = m;
+    p.part_ml[2 * at + 1] = l;
+}
+
+// 1 / l, 0 for a row that sees nothing.  With fp16 and 8 bits V is half (above).
+template <int DT, bool Q8>
+__device__ __forceinline__ float inverse(float l) {
+    return l == 0.0f ? 0.0f : (DT == DT_F16 && Q8 ? 2.0f : 1.0f) / l;
+}
+
+// Key tiles of a part: none for the last parts where there are few.
+__device__ __forceinline__ void part_of(const AttendParams& p, int total, int part, int& from, int& to) {
+    const int each = (total + p.parts - 1) / p.parts;
+    from = scalar(part * each < total ? part * each : total);
+    to = scalar(from + each < total ? from + each : total);
+}
+
+// -------------------------------------------------------------- tile kernel --
+// WAVES x 32 rows; 64 keys a stage, brought to LDS in 16 bits (through registers,
+// where 8-bit rows widen), two stages' room.  Rows of LDS are 16 bytes longer than
+// dim, so that neighbouring keys lie in different banks for every read.
+template <int DT, bool Q8, int DP, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void attend_tile_kernel(AttendParams p) {
+    constexpr int NT = WAVES * 64, KT = 64, ROWS = WAVES * 32;
+    constexpr int PITCH = DP + 8;                     // elements
+    constexpr int PIECE = Q8 ? 16 : 8;                // elements of 16 bytes of the cache
+    constexpr int PR = DP / PIECE, ALL = KT * PR;     // pieces of a row, of a stage
+    constexpr int NP = (ALL + NT - 1) / NT;           // a thread's
+    constexpr int DS = DP / 16, DO = DP / 32;
+    __shared__ __attribute__((aligned(16))) uint16_t s_k[2][KT * PITCH], s_v[2][KT * PITCH];
+    __shared__ int s_dirty[2], s_bad[2][KT];  // the stage in which V, and a key's, was not finite
+
+    const int head = blockIdx.x % p.c.heads;
+    const int rest = blockIdx.x / p.c.heads;
+    const int part = rest % p.parts;
+    // the last rows of a sequence see the most keys: first
+    const Tile t = find_tile(p, p.tiles - 1 - rest / p.parts, ROWS);
+    if (t.seq < 0) return;
+    const int wave = wave_of(), lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
+    const Row row = row_of(p, t, head * p.group, t.r0 + wave * 32 + col);
+    const Keys keys = keys_of<KT>(p, t, t.r0, ROWS);
+    int from, to;
+    part_of(p, keys.total(), part, from, to);
+    // tokens of the wave's rows, and the keys that they can see
+    const int most = t.count * p.group - 1, w0 = t.r0 + wave * 32;
+    const int i0 = w0 / p.group, i1 = (w0 + 31 < most ? w0 + 31 : most) / p.group;
+    const int wave_hi = w0 > most ? 0 : p.tree ? t.len : t.ctx + i1 + 1;
+    const int wave_lo = p.tree ? 0 : t.ctx + i0 - p.window + 1;
+    const int a0 = t.r0 / p.group, a1 = (t.r0 + ROWS - 1 < most ? t.r0 + ROWS - 1 : most) / p.group;
+
+    uint4v q[DS];
+#pragma unroll
+    for (int s = 0; s < DS; ++s) {
+        q[s] = uint4v{0, 0, 0, 0};
+        const int d = s * 16 + half * 8;
+        if (row.token >= 0 && d < p.c.dim) q[s] = load16(p.q + row.token * p.q_token + row.head * p.q_head + d * 2);
+    }
+    floatx16 o[DO];
+#pragma unroll
+    for (int i = 0; i < DO; ++i) o[i] = floatx16{};
+    float m = -INFINITY, l = 0.0f;
+
+    // staging: a thread's pieces, the same of K and V
+    const char* const kbase = p.c.k + head * p.c.ld_head;
+    const char* const vbase = p.c.v + head * p.c.ld_head;
+    uint4v rk[NP], rv[NP];
+    float sk[NP], sv[NP];
+    int pages[NP];
+    auto key_of = [&](int i, int k0) {  // a place in the sequence, whatever the tile holds
+        const int key = k0 + (i * NT + (int)threadIdx.x) / PR;
+        return key < t.len ? key : t.len - 1;
+    };
+    auto load_pages = [&](int i) {
+        const int k0 = keys.at(i) * KT;
+#pragma unroll
+        for (int j = 0; j < NP; ++j) pages[j] = page_of(p.b, t.seq, place_of(p.c, key_of(j, k0)).index);
+    };
+    auto load_rows = [&](int i) {
+        const int k0 = keys.at(i) * KT;
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+            const int at = j * NT + (int)threadIdx.x, piece = at % PR;
+            rk[j] = rv[j] = uint4v{0, 0, 0, 0};
+            sk[j] = sv[j] = 1.0f;
+            // a page that the pool does not have is read as its first
+            const int page = (unsigned)pages[j] < (unsigned)p.c.pages ? pages[j] : 0, in = place_of(p.c, key_of(j, k0)).in;
+            if ((ALL % NT == 0 || at < ALL) && piece * PIECE < p.c.dim) {
+                const long long off = page * p.c.ld_page + in * p.c.ld_token + piece * 16;
+                rk[j] = load16(kbase + off);
+                rv[j] = load16(vbase + off);
+            }
+            if constexpr (Q8) {
+                const long long soff = page * p.c.lds_page + in * p.c.lds_token + head * p.c.lds_head;
+                sk[j] = used_scale<DT, Q8>(p.c.ks[soff]);
+                sv[j] = used_scale<DT, Q8>(p.c.vs[soff]);
+            }
+        }
+    };
+    auto store_rows = [&](int i, int buf) {
+        const int k0 = keys.at(i) * KT;
+        const bool whole = all_seen<KT>(p, t, a0, a1, k0);
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+            const int at = j * NT + (int)threadIdx.x, key = at / PR, piece = at % PR;
+            if (ALL % NT && at >= ALL) continue;
+            const bool out = k0 + key >= t.len;
+            bool bad = false;
+            uint16_t* dk = &s_k[buf][key * PITCH + piece * PIECE];
+            uint16_t* dv = &s_v[buf][key * PITCH + piece * PIECE];
+#pragma unroll
+            for (int e = 0; e < (Q8 ? 2 : 1); ++e) {
+                uint4v k = Q8 ? widen8<DT>(rk[j], e, sk[j]) : rk[j];
+                uint4v v = Q8 ? widen8<DT>(rv[j], e, sv[j]) : rv[j];
+                if (!whole) {
+                    if (out) v = uint4v{0, 0, 0, 0};
+                    bad |= clear_not_finite<DT>(v);
+                }
+                *reinterpret_cast<uint4v*>(dk + 8 * e) = k;
+                *reinterpret_cast<uint4v*>(dv + 8 * e) = v;
+            }
+            if (bad) s_dirty[buf] = s_bad[buf][key] = i;
+        }
+    };
+    if (threadIdx.x < 2) s_dirty[threadIdx.x] = -1;
+    if (threadIdx.x < 2 * KT) (&s_bad[0][0])[threadIdx.x] = -1;
+    __syncthreads();
+    if (from < to) {
+        load_pages(from);
+        load_rows(from);
+        if (from + 1 < to) load_pages(from + 1);
+        store_rows(from, 0);
+    }
+    __syncthreads();
+    for (int i = from; i < to; ++i) {
+        const int buf = (i - from) & 1, k0 = keys.at(i) * KT;
+        if (i + 1 < to) {
+            load_rows(i + 1);
+            if (i + 2 < to) load_pages(i + 2);
+        }
+        const bool any = (k0 < wave_hi && k0 + KT > wave_lo) || (k0 < p.sinks && k0 < wave_hi);
+        if (any) {
+            floatx16 z[2];
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt) {
+                z[kt] = floatx16{};
+#pragma unroll
+                for (int s = 0; s < DS; ++s) {
+                    const uint4v a = *reinterpret_cast<const uint4v*>(&s_k[buf][(kt * 32 + col) * PITCH + s * 16 + half * 8]);
+                    z[kt] = mma32<DT>(a, q[s], z[kt]);
+                }
+            }
+            if (!all_seen<KT>(p, t, i0, i1, k0)) {
+                const unsigned long long bits = seen(p, t, row, k0) >> (4 * half);
+#pragma unroll
+                for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (!(bits >> (kt * 32 + 8 * (e / 4) + e % 4) & 1)) z[kt][e] = -INFINITY;
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) top = fmaxf(top, z[kt][e]);
+            top = fmaxf(top, __shfl_xor(top, 32)) * p.scale;
+            if (__any(top > m + kLag)) {
+                const float next = fmaxf(m, top);
+                const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - next);
+                l *= f;
+#pragma unroll
+                for (int d = 0; d < DO; ++d)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[d][e] *= f;
+                m = next;
+            }
+            const float base = m == -INFINITY ? 0.0f : m - p_shift<DT>();
+            uint4v w[4];  // the weights of 16 keys each
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    z[kt][e] = __builtin_amdgcn_exp2f(fmaf(z[kt][e], p.scale, -base));
+                    l += z[kt][e];
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[kt * 2 + u][e] = pack2<DT>(z[kt][8 * u + 2 * e], z[kt][8 * u + 2 * e + 1]);
+            }
+            const uint16_t* vrow = &s_v[buf][(4 * half + (lane & 15) / 4) * PITCH + 16 * ((lane >> 4) & 1) + 4 * (lane & 3)];
+#pragma unroll
+            for (int d = 0; d < DO; ++d)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint2v a = read_transposed(vrow + u * 16 * PITCH + d * 32);
+                    const uint2v b = read_transposed(vrow + (u * 16 + 8) * PITCH + d * 32);
+                    o[d] = mma32<DT>(uint4v{a[0], a[1], b[0], b[1]}, w[u], o[d]);
+                }
+            if (s_dirty[buf] == i) {
+                const unsigned long long bits = seen(p, t, row, k0);
+#pragma unroll 1
+                for (int k = 0; k < KT; ++k) {
+                    if (s_bad[buf][k] != i) continue;
+                    const CacheRow<DT, Q8> v(p, t, head, k0 + k);
+                    if (!(bits >> k & 1)) continue;
+#pragma unroll
+                    for (int d = 0; d < DO; ++d)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[d][e] += v.not_finite(d * 32 + 8 * (e / 4) + 4 * half + e % 4);
+                }
+            }
+        }
+        if (i + 1 < to) store_rows(i + 1, buf ^ 1);
+        __syncthreads();
+    }
+    l += __shfl_xor(l, 32);
+    const float inv = inverse<DT, Q8>(l);
+#pragma unroll
+    for (int d = 0; d < DO; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; e += 4)
+            put4<DT>(p, row, part, d * 32 + 2 * e + 4 * half, o[d][e], o[d][e + 1], o[d][e + 2], o[d][e + 3], inv);
+    if (half == 0) put_weight(p, row, part, m, l);
+}
+
+// --------------------------------------------------------------- row kernel --
+// Up to 16 G rows.  Memory bounds it, so a wave keeps its own keys: 32 at a time,
+// K straight to the registers of the first product, V through the wave's own
+// piece of LDS; no barrier until the waves' sums are joined.
+template <int DT, bool Q8, int DP, int G>
+__global__ __launch_bounds__(256) void attend_rows_kernel(AttendParams p) {
+    constexpr int WAVES = 4, KT = 32, ROWS = 16 * G;
+    constexpr int PITCH = DP + 8;
+    constexpr int PIECE = Q8 ? 16 : 8;
+    constexpr int PR = DP / PIECE;
+    constexpr int NK = (PR + 3) / 4;       // pieces of a key that a lane loads
+    constexpr int DS = NK * (Q8 ? 2 : 1);  // instructions of the first product
+    constexpr int DO = DP / 16;
+    constexpr int VLDS = KT * PITCH * 2, OLDS = ROWS * (DP + 4) * 4;
+    __shared__ __attribute__((aligned(16))) char s_mem[VLDS * WAVES > OLDS ? VLDS * WAVES : OLDS];
+    __shared__ float s_ml[WAVES][ROWS][2];
+
+    const int head = blockIdx.x % p.c.heads;
+    const int rest = blockIdx.x / p.c.heads;
+    const int part = rest % p.parts;
+    const Tile t = find_tile(p, p.tiles - 1 - rest / p.parts, ROWS);
+    if (t.seq < 0) return;
+    const int wave = wave_of(), lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
+    uint16_t* const s_v = reinterpret_cast<uint16_t*>(s_mem + wave * VLDS);
+    const Keys keys = keys_of<KT>(p, t, t.r0, ROWS);
+    int from, to;
+    part_of(p, keys.total(), part, from, to);
+    const int most = t.count * p.group - 1;
+    const int i0 = t.r0 / p.group, i1 = (t.r0 + ROWS - 1 < most ? t.r0 + ROWS - 1 : most) / p.group;
+
+    Row row[G];
+    uint4v q[G][DS];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        row[g] = row_of(p, t, head * p.group, t.r0 + g * 16 + col);
+#pragma unroll
+        for (int s = 0; s < DS; ++s) {
+            q[g][s] = uint4v{0, 0, 0, 0};
+            const int d = Q8 ? 16 * (4 * (s / 2) + quad) + 8 * (s % 2) : 8 * (4 * s + quad);
+            if (row[g].token >= 0 && d < p.c.dim) q[g][s] = load16(p.q + row[g].token * p.q_token + row[g].head * p.q_head + d * 2);
+        }
+    }
+    floatx4 o[G][DO];
+    float m[G], l[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+#pragma unroll
+        for (int d = 0; d < DO; ++d) o[g][d] = floatx4{};
+        m[g] = -INFINITY, l[g] = 0.0f;
+    }
+
+    const char* const kbase = p.c.k + head * p.c.ld_head;
+    const char* const vbase = p.c.v + head * p.c.ld_head;
+    // of a tile, a lane has keys col and 16 + col, and of those every fourth piece,
+    // of K and of V: 64 bytes of 16 rows a load
+    uint4v rk[2][NK], rv[2][NK];
+    float sk[2] = {1.0f, 1.0f}, sv[2] = {1.0f, 1.0f};
+    int pages[2] = {0, 0};
+    auto place = [&](int i, int h) {
+        const int key = keys.at(i) * KT + h * 16 + col;
+        return place_of(p.c, key < t.len ? key : t.len - 1);
+    };
+    auto load_pages = [&](int i) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) pages[h] = page_of(p.b, t.seq, place(i, h).index);
+    };
+    auto load_rows = [&](int i) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            // a page that the pool does not have is read as its first
+            const int page = (unsigned)pages[h] < (unsigned)p.c.pages ? pages[h] : 0, in = place(i, h).in;
+            const long long off = page * p.c.ld_page + in * p.c.ld_token + quad * 16;
+#pragma unroll
+            for (int j = 0; j < NK; ++j) {
+                rk[h][j] = rv[h][j] = uint4v{0, 0, 0, 0};
+                if ((4 * j + quad) * PIECE < p.c.dim) {
+                    rk[h][j] = load16(kbase + off + j * 64);
+                    rv[h][j] = load16(vbase + off + j * 64);
+                }
+            }
+            if constexpr (Q8) {
+                const long long soff = page * p.c.lds_page + in * p.c.lds_token + head * p.c.lds_head;
+                sk[h] = used_scale<DT, Q8>(p.c.ks[soff]);
+                sv[h] = used_scale<DT, Q8>(p.c.vs[soff]);
+            }
+        }
+    };
+
+    if (from + wave < to) {
+        load_pages(from + wave);
+        load_rows(from + wave);
+        if (from + wave + WAVES < to) load_pages(from + wave + WAVES);
+    }
+    for (int i = from + wave; i < to; i += WAVES) {
+        const int k0 = keys.at(i) * KT;
+        const bool whole = all_seen<KT>(p, t, i0, i1, k0);
+        unsigned bad = 0;  // keys whose V is not finite
+        // V to LDS, and the first product: both free their registers
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < NK; ++j) {
+                const int k = h * 16 + col;
+                if (PR % 4 && 4 * j + quad >= PR) continue;
+#pragma unroll
+                for (int e = 0; e < (Q8 ? 2 : 1); ++e) {
+                    uint4v v = Q8 ? widen8<DT>(rv[h][j], e, sv[h]) : rv[h][j];
+                    if (!whole) {
+                        if (k0 + k >= t.len) v = uint4v{0, 0, 0, 0};
+                        if (clear_not_finite<DT>(v)) bad |= 1u << k;
+                    }
+                    *reinterpret_cast<uint4v*>(s_v + k * PITCH + (4 * j + quad) * PIECE + 8 * e) = v;
+                }
+            }
+        floatx4 z[G][2];
+#pragma unroll
+        for (int g = 0; g < G; ++g) z[g][0] = z[g][1] = floatx4{};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int s = 0; s < DS; ++s) {
+                const uint4v a = Q8 ? widen8<DT>(rk[h][s / 2], s % 2, sk[h]) : rk[h][s];
+#pragma unroll
+                for (int g = 0; g < G; ++g) z[g][h] = mma16<DT>(a, q[g][s], z[g][h]);
+            }
+        if (i + WAVES < to) {
+            load_rows(i + WAVES);
+            if (i + 2 * WAVES < to) load_pages(i + 2 * WAVES);
+        }
+        uint4v w[G];
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            if (!whole) {
+                const unsigned bits = (unsigned)seen(p, t, row[g], k0) >> (4 * quad);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (!(bits >> (h * 16 + e) & 1)) z[g][h][e] = -INFINITY;
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top = fmaxf(top, z[g][h][e]);
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32)) * p.scale;
+            if (__any(top > m[g] + kLag)) {
+                const float next = fmaxf(m[g], top);
+                const float f = m[g] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[g] - next);
+                l[g] *= f;
+#pragma unroll
+                for (int d = 0; d < DO; ++d) o[g][d] *= f;
+                m[g] = next;
+            }
+            const float base = m[g] == -INFINITY ? 0.0f : m[g] - p_shift<DT>();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    z[g][h][e] = __builtin_amdgcn_exp2f(fmaf(z[g][h][e], p.scale, -base));
+                    l[g] += z[g][h][e];
+                }
+                w[g][2 * h] = pack2<DT>(z[g][h][0], z[g][h][1]);
+                w[g][2 * h + 1] = pack2<DT>(z[g][h][2], z[g][h][3]);
+            }
+        }
+        wave_fence();  // V is read by other lanes than those that wrote it
+        const uint16_t* vrow = s_v + (4 * quad + col / 4) * PITCH + 4 * (col & 3);
+#pragma unroll
+        for (int d = 0; d < DO; ++d) {
+            const uint2v a = read_transposed(vrow + d * 16), b = read_transposed(vrow + 16 * PITCH + d * 16);
+            const uint4v v = {a[0], a[1], b[0], b[1]};
+#pragma unroll
+            for (int g = 0; g < G; ++g) o[g][d] = mma16<DT>(v, w[g], o[g][d]);
+        }
+        wave_fence();  // and written anew once they have
+        if (__any(bad)) {
+#pragma unroll 1
+            for (int k = 0; k < KT; ++k) {
+                if (!__any(bad >> k & 1)) continue;
+                const CacheRow<DT, Q8> v(p, t, head, k0 + k);
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    if (!(seen(p, t, row[g], k0) >> k & 1)) continue;
+#pragma unroll
+                    for (int d = 0; d < DO; ++d)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[g][d][e] += v.not_finite(d * 16 + quad * 4 + e);
+                }
+            }
+        }
+    }
+    // the waves' sums, brought to their common maximum and added in order
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        l[g] += __shfl_xor(l[g], 16);
+        l[g] += __shfl_xor(l[g], 32);
+        if (quad == 0) {
+            s_ml[wave][g * 16 + col][0] = m[g];
+            s_ml[wave][g * 16 + col][1] = l[g];
+        }
+    }
+    __syncthreads();
+    float* const s_o = reinterpret_cast<float*>(s_mem);
+    float total[G], mx[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        mx[g] = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) mx[g] = fmaxf(mx[g], s_ml[w][g * 16 + col][0]);
+        total[g] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            const float mw = s_ml[w][g * 16 + col][0];
+            total[g] += mw == -INFINITY ? 0.0f * s_ml[w][g * 16 + col][1] : s_ml[w][g * 16 + col][1] * __builtin_amdgcn_exp2f(mw - mx[g]);
+        }
+        const float f = m[g] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[g] - mx[g]);
+#pragma unroll
+        for (int d = 0; d < DO; ++d) o[g][d] *= f;
+    }
+    for (int w = 0; w < WAVES; ++w) {
+        if (wave == w) {
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int d = 0; d < DO; ++d) {
+                    floatx4* at = reinterpret_cast<floatx4*>(s_o + (g * 16 + col) * (DP + 4) + d * 16 + quad * 4);
+                    if (w == 0) *at = o[g][d];
+                    else *at += o[g][d];
+                }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        if (g % WAVES != wave && G >= WAVES) continue;
+        const float inv = inverse<DT, Q8>(total[g]);
+#pragma unroll
+        for (int d = 0; d < DO; ++d) {
+            if (G < WAVES && (g * DO + d) % WAVES != wave) continue;
+            const floatx4 v = *reinterpret_cast<const floatx4*>(s_o + (g * 16 + col) * (DP + 4) + d * 16 + quad * 4);
+            put4<DT>(p, row[g], part, d * 16 + quad * 4, v[0], v[1], v[2], v[3], inv);
+        }
+        if (wave == g % WAVES && quad == 0) put_weight(p, row[g], part, mx[g], total[g]);
+    }
+}
+
+// --------------------------------------------------------------------- join --
+// A wave a row: the parts' sums, brought to their common maximum and added in
+// order.
+template <int DT, bool Q8>
+__global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p) {
+    const int heads = p.c.heads * p.group;
+    const long long rows = (long long)p.b.tokens * heads;
+    const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (r >= rows) return;
+    const int lane = threadIdx.x & 63, token = (int)(r / heads), head = (int)(r - (long long)token * heads);
+    if (sequence_of(p.b, token) < 0) return;  // no row: nobody wrote its parts
+    float mx = -INFINITY;
+    for (int s = 0; s < p.parts; ++s) mx = fmaxf(mx, p.part_ml[2 * (s * rows + r)]);
+    floatx4 sum = {};
+    float total = 0.0f;
+    const bool on = lane * 4 < p.c.dim;
+#pragma unroll 4
+    for (int s = 0; s < p.parts; ++s) {
+        const float m = p.part_ml[2 * (s * rows + r)], l = p.part_ml[2 * (s * rows + r) + 1];
+        floatx4 v = {};
+        if (on) v = *reinterpret_cast<const floatx4*>(p.part_o + (s * rows + r) * p.c.dim + lane * 4);
+        const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - mx);  // sums of no key are zeros
+        total += l * f;
+        sum += v * f;
+    }
+    const float inv = inverse<DT, Q8>(total);
+    if (!on) return;
+    const uint2v w = {pack2<DT>(sum[0] * inv, sum[1] * inv), pack2<DT>(sum[2] * inv, sum[3] * inv)};
+    __builtin_memcpy(p.y + token * p.y_token + head * p.y_head + lane * 8, &w, 8);
+}
+
+// ------------------------------------------------------------------- launch --
+template <int DT, bool Q8, int DP>
+void launch_dim(const AttendPlan& plan, const AttendParams& p, hipStream_t stream) {
+    const dim3 grid((unsigned)((long long)p.tiles * p.parts * p.c.heads));
+    constexpr int WAVES = DP > 128 ? 4 : 8;
+    if (plan.form == ATT_TILE)
+        attend_tile_kernel<DT, Q8, DP, WAVES><<<grid, dim3(WAVES * 64), 0, stream>>>(p);
+    else if (plan.form == ATT_ROW16)
+        attend_rows_kernel<DT, Q8, DP, 1><<<grid, dim3(256), 0, stream>>>(p);
+    else if (plan.form == ATT_ROW32 || DP > 128)
+        attend_rows_kernel<DT, Q8, DP, 2><<<grid, dim3(256), 0, stream>>>(p);
+    else
+        attend_rows_kernel<DT, Q8, DP, (DP > 128 ? 2 : 4)><<<grid, dim3(256), 0, stream>>>(p);
+}
+
+template <int DT, bool Q8>
+hipError_t launch_type(const AttendPlan& plan, const AttendParams& p, hipStream_t stream) {
+    if (p.c.dim <= 64) launch_dim<DT, Q8, 64>(plan, p, stream);
+    else if (p.c.dim <= 128) launch_dim<DT, Q8, 128>(plan, p, stream);
+    else launch_dim<DT, Q8, 256>(plan, p, stream);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.parts <= 1) return e;
+    const long long rows = (long long)p.b.tokens * p.c.heads * p.group;
+    attend_join_kernel<DT, Q8><<<dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream>>>(p);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attend(const AttendPlan& plan, const AttendParams& p, int cache_dt, int dt, hipStream_t stream) {
+    (void)hipGetLastError();
+    if (dt == DT_F16) return cache_dt == DT_E4M3 ? launch_type<DT_F16, true>(plan, p, stream) : launch_type<DT_F16, false>(plan, p, stream);
+    return cache_dt == DT_E4M3 ? launch_type<DT_BF16, true>(plan, p, stream) : launch_type<DT_BF16, false>(plan, p, stream);
+}
+
+}  // namespace ct
