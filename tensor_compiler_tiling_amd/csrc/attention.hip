@@ -106,6 +106,30 @@ __device__ __forceinline__ uint2v read_transposed(const uint16_t* p) {
 // hardware runs them in order.
 __device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local"); }
 
+// A value that the compiler takes for new here: it is made at this place, and what
+// a rare path makes of it is not made ahead of the loop, where it would be kept in
+// registers.
+template <typename T>
+__device__ __forceinline__ T in_place(T v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// The greater of a lane's value and that of the lane 32 away.
+__device__ __forceinline__ float max_of_halves(float v) {
+    typedef unsigned int pair __attribute__((ext_vector_type(2)));
+    const pair r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// Ends a turn of the tile kernel: what was written to LDS is there, and no access
+// of it crosses (loads of global memory may be on their way).
+__device__ __forceinline__ void end_turn() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // A value that all lanes share, as a scalar.  What is the wave's own (its index,
 // its keys, its loop's ends) goes through this, so that the branches on it are
 // scalar too.  With conditions as masks, where registers were short, the compiler
@@ -173,9 +197,9 @@ __device__ __forceinline__ Tile find_tile(const AttendParams& p, int tile, int r
             before += __shfl(upto, 63);
         }
     }
-    if (t.seq < 0) return t;
     t.seq = scalar(t.seq);
     t.r0 = scalar(t.r0);
+    if (t.seq < 0) return t;
     const Span sp = span_of(p.b, t.seq);
     t.first = scalar(sp.first);
     t.count = scalar(sp.count);
@@ -293,7 +317,7 @@ struct CacheRow {
         v = p.c.v + page * p.c.ld_page + at.in * p.c.ld_token + head * p.c.ld_head;
     }
     __device__ __forceinline__ float not_finite(int d) const {
-        if (d >= dim) return 0.0f;
+        d = d < dim ? d : dim - 1;  // what lies beyond is not stored
         float f;
         if constexpr (Q8)
             f = (v[d] & 0x7f) == 0x7f ? __builtin_nanf("") : 0.0f;
@@ -339,19 +363,22 @@ __device__ __forceinline__ void part_of(const AttendParams& p, int total, int pa
 }
 
 // -------------------------------------------------------------- tile kernel --
-// WAVES x 32 rows; 64 keys a stage, brought to LDS in 16 bits (through registers,
-// where 8-bit rows widen), two stages' room.  Rows of LDS are 16 bytes longer than
-// dim, so that neighbouring keys lie in different banks for every read.
-template <int DT, bool Q8, int DP, int WAVES>
-__global__ __launch_bounds__(WAVES * 64) void attend_tile_kernel(AttendParams p) {
-    constexpr int NT = WAVES * 64, KT = 64, ROWS = WAVES * 32;
-    constexpr int PITCH = DP + 8;                     // elements
-    constexpr int PIECE = Q8 ? 16 : 8;                // elements of 16 bytes of the cache
-    constexpr int PR = DP / PIECE, ALL = KT * PR;     // pieces of a row, of a stage
-    constexpr int NP = (ALL + NT - 1) / NT;           // a thread's
+// WAVES x 32 rows; KT keys a stage, brought to LDS in 16 bits (through registers,
+// where 8-bit rows widen), two stages' room.  Rows of K in LDS are 16 bytes longer
+// than dim: 16 neighbouring keys, read 16 bytes each, then cover all 64 banks.  Those
+// of V lie 64 bytes (mod 256) apart: a transposing read takes 64 bytes of 8 keys.
+template <int DT, bool Q8, int DP, int WAVES, int KT>
+__global__ __launch_bounds__(WAVES * 64, (DP > 128 ? 1 : 2)) void attend_tile_kernel(AttendParams p) {
+    constexpr int NT = WAVES * 64, ROWS = WAVES * 32, NK = KT / 32;
+    constexpr int KP = DP + 8, VP = DP == 96 ? DP : DP + 32;  // elements
+    constexpr int PIECE = Q8 ? 16 : 8;             // elements of 16 bytes of the cache
+    constexpr int PR = DP / PIECE, ALL = KT * PR;  // pieces of a row, of a stage
+    constexpr int NP = (ALL + NT - 1) / NT;        // a thread's
     constexpr int DS = DP / 16, DO = DP / 32;
-    __shared__ __attribute__((aligned(16))) uint16_t s_k[2][KT * PITCH], s_v[2][KT * PITCH];
+    __shared__ __attribute__((aligned(16))) uint16_t s_k[2][KT * KP], s_v[2][KT * VP];
     __shared__ int s_dirty[2], s_bad[2][KT];  // the stage in which V, and a key's, was not finite
+    __shared__ long long s_at[4][KT];         // where a stage's keys lie
+    __shared__ float s_scale[Q8 ? 4 : 1][KT][2];
 
     const int head = blockIdx.x % p.c.heads;
     const int rest = blockIdx.x / p.c.heads;
@@ -366,10 +393,10 @@ __global__ __launch_bounds__(WAVES * 64) void attend_tile_kernel(AttendParams p)
     part_of(p, keys.total(), part, from, to);
     // tokens of the wave's rows, and the keys that they can see
     const int most = t.count * p.group - 1, w0 = t.r0 + wave * 32;
-    const int i0 = w0 / p.group, i1 = (w0 + 31 < most ? w0 + 31 : most) / p.group;
+    const int i0 = scalar(w0 / p.group), i1 = scalar((w0 + 31 < most ? w0 + 31 : most) / p.group);
     const int wave_hi = w0 > most ? 0 : p.tree ? t.len : t.ctx + i1 + 1;
     const int wave_lo = p.tree ? 0 : t.ctx + i0 - p.window + 1;
-    const int a0 = t.r0 / p.group, a1 = (t.r0 + ROWS - 1 < most ? t.r0 + ROWS - 1 : most) / p.group;
+    const int a0 = scalar(t.r0 / p.group), a1 = scalar((t.r0 + ROWS - 1 < most ? t.r0 + ROWS - 1 : most) / p.group);
 
     uint4v q[DS];
 #pragma unroll
@@ -378,163 +405,253 @@ __global__ __launch_bounds__(WAVES * 64) void attend_tile_kernel(AttendParams p)
         const int d = s * 16 + half * 8;
         if (row.token >= 0 && d < p.c.dim) q[s] = load16(p.q + row.token * p.q_token + row.head * p.q_head + d * 2);
     }
+#pragma unroll
+    for (int s = 0; s < DS; ++s) q[s] = in_place(q[s]);  // waited for here, not in the loop
     floatx16 o[DO];
 #pragma unroll
     for (int i = 0; i < DO; ++i) o[i] = floatx16{};
     float m = -INFINITY, l = 0.0f;
 
-    // staging: a thread's pieces, the same of K and V
+    // Staging.  The workgroup's first wave looks up where a stage's keys lie, a key a
+    // lane, some turns ahead, and leaves their places (and scales) in LDS: the page of
+    // stage i + 4 is asked for, its place for i + 3 made, its scales for i + 2 there.
     const char* const kbase = p.c.k + head * p.c.ld_head;
     const char* const vbase = p.c.v + head * p.c.ld_head;
-    uint4v rk[NP], rv[NP];
-    float sk[NP], sv[NP];
-    int pages[NP];
-    auto key_of = [&](int i, int k0) {  // a place in the sequence, whatever the tile holds
-        const int key = k0 + (i * NT + (int)threadIdx.x) / PR;
-        return key < t.len ? key : t.len - 1;
+    const float* const ksbase = Q8 ? p.c.ks + head * p.c.lds_head : nullptr;
+    const float* const vsbase = Q8 ? p.c.vs + head * p.c.lds_head : nullptr;
+    int page = 0;
+    float ks = 1.0f, vs = 1.0f;
+    auto place = [&](int i) {
+        const int key = keys.at(i) * KT + in_place(lane) % KT;
+        return place_of(p.c, key < t.len ? key : t.len - 1);
     };
-    auto load_pages = [&](int i) {
-        const int k0 = keys.at(i) * KT;
-#pragma unroll
-        for (int j = 0; j < NP; ++j) pages[j] = page_of(p.b, t.seq, place_of(p.c, key_of(j, k0)).index);
+    auto ask_page = [&](int i) {
+        if (i < to) page = page_of(p.b, t.seq, place(i).index);
     };
-    auto load_rows = [&](int i) {
-        const int k0 = keys.at(i) * KT;
-#pragma unroll
-        for (int j = 0; j < NP; ++j) {
-            const int at = j * NT + (int)threadIdx.x, piece = at % PR;
-            rk[j] = rv[j] = uint4v{0, 0, 0, 0};
-            sk[j] = sv[j] = 1.0f;
-            // a page that the pool does not have is read as its first
-            const int page = (unsigned)pages[j] < (unsigned)p.c.pages ? pages[j] : 0, in = place_of(p.c, key_of(j, k0)).in;
-            if ((ALL % NT == 0 || at < ALL) && piece * PIECE < p.c.dim) {
-                const long long off = page * p.c.ld_page + in * p.c.ld_token + piece * 16;
-                rk[j] = load16(kbase + off);
-                rv[j] = load16(vbase + off);
-            }
-            if constexpr (Q8) {
-                const long long soff = page * p.c.lds_page + in * p.c.lds_token + head * p.c.lds_head;
-                sk[j] = used_scale<DT, Q8>(p.c.ks[soff]);
-                sv[j] = used_scale<DT, Q8>(p.c.vs[soff]);
-            }
+    auto put_place = [&](int i) {
+        if (i >= to) return;
+        // a page that the pool does not have is read as its first
+        const int pg = (unsigned)page < (unsigned)p.c.pages ? page : 0, in = place(i).in;
+        s_at[(i - from) & 3][in_place(lane) % KT] = pg * p.c.ld_page + in * p.c.ld_token;
+        if constexpr (Q8) {
+            const long long soff = pg * p.c.lds_page + in * p.c.lds_token;
+            ks = used_scale<DT, Q8>(ksbase[soff]);
+            vs = used_scale<DT, Q8>(vsbase[soff]);
         }
     };
-    auto store_rows = [&](int i, int buf) {
-        const int k0 = keys.at(i) * KT;
+    auto put_scales = [&](int i) {
+        if constexpr (Q8) {
+            if (i >= to) return;
+            s_scale[(i - from) & 3][lane % KT][0] = ks;
+            s_scale[(i - from) & 3][lane % KT][1] = vs;
+        }
+    };
+    auto look_up = [&](int i) {
+        put_scales(i + 2);
+        put_place(i + 3);
+        ask_page(i + 4);
+    };
+    // A thread's pieces of K and of V: piece j of key key_of(j).
+    constexpr bool EVEN = NT % PR == 0;
+    uint4v rk[NP], rv[NP];
+    const int key0 = (int)threadIdx.x / PR, piece0 = (int)threadIdx.x % PR;
+    auto key_of = [&](int j) { return EVEN ? key0 + j * (NT / PR) : (j * NT + (int)threadIdx.x) / PR; };
+    auto piece_of = [&](int j) { return EVEN ? piece0 : (j * NT + (int)threadIdx.x) % PR; };
+#pragma unroll
+    for (int j = 0; j < NP; ++j) rk[j] = rv[j] = uint4v{0, 0, 0, 0};  // those past dim stay so
+    auto load_rows = [&](int i, const char* base, uint4v (&r)[NP]) {
+        long long at[NP];
+#pragma unroll
+        for (int j = 0; j < NP; ++j) at[j] = s_at[(i - from) & 3][key_of(j) % KT] + piece_of(j) * 16;
+        if constexpr (EVEN && ALL % NT == 0) {
+            if (piece0 * PIECE < p.c.dim) {
+#pragma unroll
+                for (int j = 0; j < NP; ++j) r[j] = load16(base + at[j]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NP; ++j)
+                if (key_of(j) < KT && piece_of(j) * PIECE < p.c.dim) r[j] = load16(base + at[j]);
+        }
+    };
+    auto store_k = [&](int i) {
+        uint16_t* const to_k = s_k[(i - from) & 1];
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+            if (ALL % NT && key_of(j) >= KT) continue;
+            const float f = Q8 ? s_scale[(i - from) & 3][key_of(j)][0] : 1.0f;
+#pragma unroll
+            for (int e = 0; e < (Q8 ? 2 : 1); ++e)
+                *reinterpret_cast<uint4v*>(to_k + key_of(j) * KP + piece_of(j) * PIECE + 8 * e) = Q8 ? widen8<DT>(rk[j], e, f) : rk[j];
+        }
+    };
+    auto store_v = [&](int i) {
+        const int k0 = keys.at(i) * KT, buf = (i - from) & 1;
         const bool whole = all_seen<KT>(p, t, a0, a1, k0);
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
-            const int at = j * NT + (int)threadIdx.x, key = at / PR, piece = at % PR;
-            if (ALL % NT && at >= ALL) continue;
-            const bool out = k0 + key >= t.len;
+            if (ALL % NT && key_of(j) >= KT) continue;
+            const float f = Q8 ? s_scale[(i - from) & 3][key_of(j)][1] : 1.0f;
             bool bad = false;
-            uint16_t* dk = &s_k[buf][key * PITCH + piece * PIECE];
-            uint16_t* dv = &s_v[buf][key * PITCH + piece * PIECE];
 #pragma unroll
             for (int e = 0; e < (Q8 ? 2 : 1); ++e) {
-                uint4v k = Q8 ? widen8<DT>(rk[j], e, sk[j]) : rk[j];
-                uint4v v = Q8 ? widen8<DT>(rv[j], e, sv[j]) : rv[j];
+                uint4v v = Q8 ? widen8<DT>(rv[j], e, f) : rv[j];
                 if (!whole) {
-                    if (out) v = uint4v{0, 0, 0, 0};
+                    if (k0 + key_of(j) >= t.len) v = uint4v{0, 0, 0, 0};
                     bad |= clear_not_finite<DT>(v);
                 }
-                *reinterpret_cast<uint4v*>(dk + 8 * e) = k;
-                *reinterpret_cast<uint4v*>(dv + 8 * e) = v;
+                *reinterpret_cast<uint4v*>(s_v[buf] + key_of(j) * VP + piece_of(j) * PIECE + 8 * e) = v;
             }
-            if (bad) s_dirty[buf] = s_bad[buf][key] = i;
+            if (bad) s_dirty[buf] = s_bad[buf][key_of(j)] = i;
         }
     };
     if (threadIdx.x < 2) s_dirty[threadIdx.x] = -1;
     if (threadIdx.x < 2 * KT) (&s_bad[0][0])[threadIdx.x] = -1;
-    __syncthreads();
-    if (from < to) {
-        load_pages(from);
-        load_rows(from);
-        if (from + 1 < to) load_pages(from + 1);
-        store_rows(from, 0);
-    }
-    __syncthreads();
-    for (int i = from; i < to; ++i) {
-        const int buf = (i - from) & 1, k0 = keys.at(i) * KT;
-        if (i + 1 < to) {
-            load_rows(i + 1);
-            if (i + 2 < to) load_pages(i + 2);
+
+    // A turn: the first product of stage i and the second of stage i - 1, in one run;
+    // the weights of stage i; then K of stage i + 1 and V of stage i to LDS, from
+    // registers that were loaded in the turn before.  One barrier a turn.  A SIMD's two
+    // waves soon run against each other, one's products beside the other's weights.
+    //
+    // Scheduling barriers hold the order of the run: each product has its operand read
+    // from LDS AHEAD products before.  Left to itself the compiler reads, waits and
+    // multiplies.
+    constexpr int AHEAD = 6, FIRST = NK * DS, SECOND = 2 * NK * DO;
+    floatx16 z[NK];
+    uint4v w[2 * NK];  // the weights of 16 keys each
+    auto products = [&](int i, auto with_first, auto with_second) {
+        constexpr int BEGIN = decltype(with_first)::value ? 0 : FIRST, END = decltype(with_second)::value ? FIRST + SECOND : FIRST;
+        const int ln = in_place(lane);  // made anew: registers are short
+        const uint16_t* const krow = &s_k[(i - from) & 1][(ln & 31) * KP + (ln >> 5) * 8];
+        const uint16_t* const vrow = &s_v[(i - from + 1) & 1][(4 * (ln >> 5) + (ln & 15) / 4) * VP + 16 * ((ln >> 4) & 1) + 4 * (ln & 3)];
+        uint4v f[AHEAD];
+        auto read = [&](int n) {
+            if (n < FIRST) {
+                f[n % AHEAD] = *reinterpret_cast<const uint4v*>(krow + n / DS * 32 * KP + n % DS * 16);
+            } else {
+                const uint16_t* const at = vrow + (n - FIRST) / DO * 16 * VP + (n - FIRST) % DO * 32;
+                const uint2v a = read_transposed(at), b = read_transposed(at + 8 * VP);
+                f[n % AHEAD] = uint4v{a[0], a[1], b[0], b[1]};
+            }
+        };
+        if constexpr (BEGIN == 0) {
+#pragma unroll
+            for (int kt = 0; kt < NK; ++kt) z[kt] = floatx16{};
         }
-        const bool any = (k0 < wave_hi && k0 + KT > wave_lo) || (k0 < p.sinks && k0 < wave_hi);
-        if (any) {
-            floatx16 z[2];
 #pragma unroll
-            for (int kt = 0; kt < 2; ++kt) {
-                z[kt] = floatx16{};
+        for (int n = BEGIN; n < BEGIN + AHEAD; ++n) read(n);
 #pragma unroll
-                for (int s = 0; s < DS; ++s) {
-                    const uint4v a = *reinterpret_cast<const uint4v*>(&s_k[buf][(kt * 32 + col) * PITCH + s * 16 + half * 8]);
-                    z[kt] = mma32<DT>(a, q[s], z[kt]);
-                }
-            }
-            if (!all_seen<KT>(p, t, i0, i1, k0)) {
-                const unsigned long long bits = seen(p, t, row, k0) >> (4 * half);
+        for (int n = BEGIN; n < END; ++n) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (n < FIRST) z[n / DS] = mma32<DT>(f[n % AHEAD], q[n % DS], z[n / DS]);
+            else o[(n - FIRST) % DO] = mma32<DT>(f[n % AHEAD], w[(n - FIRST) / DO], o[(n - FIRST) % DO]);
+            if (n + AHEAD < END) read(n + AHEAD);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto weights = [&](int i) {
+        const int k0 = keys.at(i) * KT;
+        if (!all_seen<KT>(p, t, i0, i1, k0)) {
+            const unsigned long long bits = seen(p, t, row, k0) >> (4 * half);
 #pragma unroll
-                for (int kt = 0; kt < 2; ++kt)
+            for (int kt = 0; kt < NK; ++kt)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (!(bits >> (kt * 32 + 8 * (e / 4) + e % 4) & 1)) z[kt][e] = -INFINITY;
-            }
-            float top = -INFINITY;
+                for (int e = 0; e < 16; ++e)
+                    if (!(bits >> (kt * 32 + 8 * (e / 4) + e % 4) & 1)) z[kt][e] = -INFINITY;
+        }
+        float top = -INFINITY;
 #pragma unroll
-            for (int kt = 0; kt < 2; ++kt)
+        for (int kt = 0; kt < NK; ++kt)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) top = fmaxf(top, z[kt][e]);
-            top = fmaxf(top, __shfl_xor(top, 32)) * p.scale;
-            if (__any(top > m + kLag)) {
-                const float next = fmaxf(m, top);
-                const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - next);
-                l *= f;
-#pragma unroll
-                for (int d = 0; d < DO; ++d)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[d][e] *= f;
-                m = next;
-            }
-            const float base = m == -INFINITY ? 0.0f : m - p_shift<DT>();
-            uint4v w[4];  // the weights of 16 keys each
-#pragma unroll
-            for (int kt = 0; kt < 2; ++kt) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    z[kt][e] = __builtin_amdgcn_exp2f(fmaf(z[kt][e], p.scale, -base));
-                    l += z[kt][e];
-                }
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) w[kt * 2 + u][e] = pack2<DT>(z[kt][8 * u + 2 * e], z[kt][8 * u + 2 * e + 1]);
-            }
-            const uint16_t* vrow = &s_v[buf][(4 * half + (lane & 15) / 4) * PITCH + 16 * ((lane >> 4) & 1) + 4 * (lane & 3)];
+            for (int e = 0; e < 16; ++e) top = fmaxf(top, z[kt][e]);
+        top = max_of_halves(top) * p.scale;
+        if (__any(top > m + kLag)) {
+            const float next = fmaxf(m, top);
+            // at least the least normal number: what is infinite stays so
+            const float fall = m == -INFINITY ? 1.0f : fmaxf(__builtin_amdgcn_exp2f(m - next), 0x1p-126f);
+            l *= fall;
 #pragma unroll
             for (int d = 0; d < DO; ++d)
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const uint2v a = read_transposed(vrow + u * 16 * PITCH + d * 32);
-                    const uint2v b = read_transposed(vrow + (u * 16 + 8) * PITCH + d * 32);
-                    o[d] = mma32<DT>(uint4v{a[0], a[1], b[0], b[1]}, w[u], o[d]);
-                }
-            if (s_dirty[buf] == i) {
-                const unsigned long long bits = seen(p, t, row, k0);
-#pragma unroll 1
-                for (int k = 0; k < KT; ++k) {
-                    if (s_bad[buf][k] != i) continue;
-                    const CacheRow<DT, Q8> v(p, t, head, k0 + k);
-                    if (!(bits >> k & 1)) continue;
-#pragma unroll
-                    for (int d = 0; d < DO; ++d)
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) o[d][e] += v.not_finite(d * 32 + 8 * (e / 4) + 4 * half + e % 4);
-                }
-            }
+                for (int e = 0; e < 16; ++e) o[d][e] *= fall;
+            m = next;
         }
-        if (i + 1 < to) store_rows(i + 1, buf ^ 1);
-        __syncthreads();
+        const float base = m == -INFINITY ? 0.0f : m - p_shift<DT>();
+#pragma unroll
+        for (int kt = 0; kt < NK; ++kt)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                z[kt][e] = __builtin_amdgcn_exp2f(fmaf(z[kt][e], p.scale, -base));
+                l += z[kt][e];
+            }
+#pragma unroll
+        for (int u = 0; u < 2 * NK; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[u][e] = pack2<DT>(z[u / 2][8 * (u % 2) + 2 * e], z[u / 2][8 * (u % 2) + 2 * e + 1]);
+    };
+    // what of stage i is not finite
+    auto add_not_finite = [&](int i) {
+        const int buf = (i - from) & 1;
+        if (s_dirty[buf] != i) return;
+        const int k0 = keys.at(i) * KT;
+        const unsigned long long bits = seen(p, t, row, k0);
+#pragma unroll 1
+        for (int k = 0; k < KT; ++k) {
+            if (s_bad[buf][k] != i) continue;
+            const CacheRow<DT, Q8> v(p, t, head, k0 + k);
+            if (!(bits >> k & 1)) continue;
+            const int d0 = in_place(4 * half);
+#pragma unroll
+            for (int d = 0; d < DO; ++d)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[d][e] = in_place(o[d][e] + v.not_finite(d0 + d * 32 + 8 * (e / 4) + e % 4));
+        }
+    };
+    // K of stage i + 1 and V of stage i, whose room is free while stage i's turn lasts
+    auto load = [&](int i) {
+        if (i < to) load_rows(i, vbase, rv);
+        if (i + 1 < to) load_rows(i + 1, kbase, rk);
+    };
+    auto store = [&](int i) {
+        if (i + 1 < to) store_k(i + 1);
+        if (i < to) store_v(i);
+    };
+    if (from < to && wave == 0) {
+        // the turns before the first
+        ask_page(from);
+        put_place(from);
+        ask_page(from + 1);
+        put_scales(from);
+        put_place(from + 1);
+        ask_page(from + 2);
+        look_up(from - 1);
+    }
+    __syncthreads();
+    if (from < to) {
+        load_rows(from, kbase, rk);
+        store_k(from);
+        load(from);
+    }
+    __syncthreads();
+    const bool idle = w0 > most;  // no rows
+    for (int i = from; i < to; ++i) {
+        if (wave == 0) look_up(i);
+        if (!idle) {
+            if (i > from) {
+                products(i, std::true_type{}, std::true_type{});
+                add_not_finite(i - 1);
+            } else {
+                products(i, std::true_type{}, std::false_type{});
+            }
+            weights(i);
+        }
+        store(i);
+        load(i + 1);
+        end_turn();
+    }
+    if (from < to && !idle) {
+        products(to, std::false_type{}, std::true_type{});
+        add_not_finite(to - 1);
     }
     l += __shfl_xor(l, 32);
     const float inv = inverse<DT, Q8>(l);
@@ -553,7 +670,7 @@ __global__ __launch_bounds__(WAVES * 64) void attend_tile_kernel(AttendParams p)
 template <int DT, bool Q8, int DP, int G>
 __global__ __launch_bounds__(256) void attend_rows_kernel(AttendParams p) {
     constexpr int WAVES = 4, KT = 32, ROWS = 16 * G;
-    constexpr int PITCH = DP + 8;
+    constexpr int PITCH = DP + 16;         // of V in LDS: a transposing read takes 32 bytes of 16 keys
     constexpr int PIECE = Q8 ? 16 : 8;
     constexpr int PR = DP / PIECE;
     constexpr int NK = (PR + 3) / 4;       // pieces of a key that a lane loads
@@ -731,10 +848,11 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendParams p) {
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
                     if (!(seen(p, t, row[g], k0) >> k & 1)) continue;
+                    const int d0 = in_place(4 * quad);
 #pragma unroll
                     for (int d = 0; d < DO; ++d)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) o[g][d][e] += v.not_finite(d * 16 + quad * 4 + e);
+                        for (int e = 0; e < 4; ++e) o[g][d][e] = in_place(o[g][d][e] + v.not_finite(d0 + d * 16 + e));
                 }
             }
         }
@@ -831,7 +949,7 @@ void launch_dim(const AttendPlan& plan, const AttendParams& p, hipStream_t strea
     const dim3 grid((unsigned)((long long)p.tiles * p.parts * p.c.heads));
     constexpr int WAVES = DP > 128 ? 4 : 8;
     if (plan.form == ATT_TILE)
-        attend_tile_kernel<DT, Q8, DP, WAVES><<<grid, dim3(WAVES * 64), 0, stream>>>(p);
+        attend_tile_kernel<DT, Q8, DP, WAVES, 64><<<grid, dim3(WAVES * 64), 0, stream>>>(p);
     else if (plan.form == ATT_ROW16)
         attend_rows_kernel<DT, Q8, DP, 1><<<grid, dim3(256), 0, stream>>>(p);
     else if (plan.form == ATT_ROW32 || DP > 128)
