@@ -377,8 +377,8 @@ __global__ __launch_bounds__(WAVES * 64, (DP > 128 ? 1 : 2)) void attend_tile_ke
     constexpr int DS = DP / 16, DO = DP / 32;
     __shared__ __attribute__((aligned(16))) uint16_t s_k[2][KT * KP], s_v[2][KT * VP];
     __shared__ int s_dirty[2], s_bad[2][KT];  // the stage in which V, and a key's, was not finite
-    __shared__ long long s_at[4][KT];         // where a stage's keys lie
-    __shared__ float s_scale[Q8 ? 4 : 1][KT][2];
+    __shared__ long long s_at[4 * WAVES][KT];  // where a stage's keys lie
+    __shared__ float s_scale[Q8 ? 2 * WAVES : 1][KT][2];
 
     const int head = blockIdx.x % p.c.heads;
     const int rest = blockIdx.x / p.c.heads;
@@ -412,9 +412,10 @@ __global__ __launch_bounds__(WAVES * 64, (DP > 128 ? 1 : 2)) void attend_tile_ke
     for (int i = 0; i < DO; ++i) o[i] = floatx16{};
     float m = -INFINITY, l = 0.0f;
 
-    // Staging.  The workgroup's first wave looks up where a stage's keys lie, a key a
-    // lane, some turns ahead, and leaves their places (and scales) in LDS: the page of
-    // stage i + 4 is asked for, its place for i + 3 made, its scales for i + 2 there.
+    // Staging.  Where a stage's keys lie is looked up some blocks of WAVES stages ahead,
+    // a stage a wave and a key a lane, and left in LDS with the scales: at the first
+    // turn of block b its waves ask for the pages of block b + 3, make the places of
+    // b + 2 and have the scales of b + 1.
     const char* const kbase = p.c.k + head * p.c.ld_head;
     const char* const vbase = p.c.v + head * p.c.ld_head;
     const float* const ksbase = Q8 ? p.c.ks + head * p.c.lds_head : nullptr;
@@ -432,7 +433,7 @@ __global__ __launch_bounds__(WAVES * 64, (DP > 128 ? 1 : 2)) void attend_tile_ke
         if (i >= to) return;
         // a page that the pool does not have is read as its first
         const int pg = (unsigned)page < (unsigned)p.c.pages ? page : 0, in = place(i).in;
-        s_at[(i - from) & 3][in_place(lane) % KT] = pg * p.c.ld_page + in * p.c.ld_token;
+        s_at[(i - from) % (4 * WAVES)][in_place(lane) % KT] = pg * p.c.ld_page + in * p.c.ld_token;
         if constexpr (Q8) {
             const long long soff = pg * p.c.lds_page + in * p.c.lds_token;
             ks = used_scale<DT, Q8>(ksbase[soff]);
@@ -442,14 +443,14 @@ __global__ __launch_bounds__(WAVES * 64, (DP > 128 ? 1 : 2)) void attend_tile_ke
     auto put_scales = [&](int i) {
         if constexpr (Q8) {
             if (i >= to) return;
-            s_scale[(i - from) & 3][lane % KT][0] = ks;
-            s_scale[(i - from) & 3][lane % KT][1] = vs;
+            s_scale[(i - from) % (2 * WAVES)][lane % KT][0] = ks;
+            s_scale[(i - from) % (2 * WAVES)][lane % KT][1] = vs;
         }
     };
-    auto look_up = [&](int i) {
-        put_scales(i + 2);
-        put_place(i + 3);
-        ask_page(i + 4);
+    auto look_up = [&](int i) {  // i: a block's first stage
+        put_scales(i + WAVES + wave);
+        put_place(i + 2 * WAVES + wave);
+        ask_page(i + 3 * WAVES + wave);
     };
     // A thread's pieces of K and of V: piece j of key key_of(j).
     constexpr bool EVEN = NT % PR == 0;
@@ -462,7 +463,7 @@ __global__ __launch_bounds__(WAVES * 64, (DP > 128 ? 1 : 2)) void attend_tile_ke
     auto load_rows = [&](int i, const char* base, uint4v (&r)[NP]) {
         long long at[NP];
 #pragma unroll
-        for (int j = 0; j < NP; ++j) at[j] = s_at[(i - from) & 3][key_of(j) % KT] + piece_of(j) * 16;
+        for (int j = 0; j < NP; ++j) at[j] = s_at[(i - from) % (4 * WAVES)][key_of(j) % KT] + piece_of(j) * 16;
         if constexpr (EVEN && ALL % NT == 0) {
             if (piece0 * PIECE < p.c.dim) {
 #pragma unroll
@@ -479,7 +480,7 @@ __global__ __launch_bounds__(WAVES * 64, (DP > 128 ? 1 : 2)) void attend_tile_ke
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
             if (ALL % NT && key_of(j) >= KT) continue;
-            const float f = Q8 ? s_scale[(i - from) & 3][key_of(j)][0] : 1.0f;
+            const float f = Q8 ? s_scale[(i - from) % (2 * WAVES)][key_of(j)][0] : 1.0f;
 #pragma unroll
             for (int e = 0; e < (Q8 ? 2 : 1); ++e)
                 *reinterpret_cast<uint4v*>(to_k + key_of(j) * KP + piece_of(j) * PIECE + 8 * e) = Q8 ? widen8<DT>(rk[j], e, f) : rk[j];
@@ -491,7 +492,7 @@ __global__ __launch_bounds__(WAVES * 64, (DP > 128 ? 1 : 2)) void attend_tile_ke
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
             if (ALL % NT && key_of(j) >= KT) continue;
-            const float f = Q8 ? s_scale[(i - from) & 3][key_of(j)][1] : 1.0f;
+            const float f = Q8 ? s_scale[(i - from) % (2 * WAVES)][key_of(j)][1] : 1.0f;
             bool bad = false;
 #pragma unroll
             for (int e = 0; e < (Q8 ? 2 : 1); ++e) {
@@ -616,16 +617,13 @@ __global__ __launch_bounds__(WAVES * 64, (DP > 128 ? 1 : 2)) void attend_tile_ke
         if (i + 1 < to) store_k(i + 1);
         if (i < to) store_v(i);
     };
-    if (from < to && wave == 0) {
-        // the turns before the first
-        ask_page(from);
-        put_place(from);
-        ask_page(from + 1);
-        put_scales(from);
-        put_place(from + 1);
-        ask_page(from + 2);
-        look_up(from - 1);
-    }
+    // the blocks before the first
+    ask_page(from + wave);
+    put_place(from + wave);
+    ask_page(from + WAVES + wave);
+    put_scales(from + wave);
+    put_place(from + WAVES + wave);
+    ask_page(from + 2 * WAVES + wave);
     __syncthreads();
     if (from < to) {
         load_rows(from, kbase, rk);
@@ -635,7 +633,7 @@ __global__ __launch_bounds__(WAVES * 64, (DP > 128 ? 1 : 2)) void attend_tile_ke
     __syncthreads();
     const bool idle = w0 > most;  // no rows
     for (int i = from; i < to; ++i) {
-        if (wave == 0) look_up(i);
+        if ((i - from) % WAVES == 0) look_up(i);
         if (!idle) {
             if (i > from) {
                 products(i, std::true_type{}, std::true_type{});
