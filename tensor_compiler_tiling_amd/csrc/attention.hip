@@ -405,8 +405,6 @@ __global__ __launch_bounds__(WAVES * 64, (DP > 128 ? 1 : 2)) void attend_tile_ke
         const int d = s * 16 + half * 8;
         if (row.token >= 0 && d < p.c.dim) q[s] = load16(p.q + row.token * p.q_token + row.head * p.q_head + d * 2);
     }
-#pragma unroll
-    for (int s = 0; s < DS; ++s) q[s] = in_place(q[s]);  // waited for here, not in the loop
     floatx16 o[DO];
 #pragma unroll
     for (int i = 0; i < DO; ++i) o[i] = floatx16{};
@@ -426,10 +424,8 @@ __global__ __launch_bounds__(WAVES * 64, (DP > 128 ? 1 : 2)) void attend_tile_ke
         const int key = keys.at(i) * KT + in_place(lane) % KT;
         return place_of(p.c, key < t.len ? key : t.len - 1);
     };
-    auto ask_page = [&](int i) {
-        if (i < to) page = page_of(p.b, t.seq, place(i).index);
-    };
-    auto put_place = [&](int i) {
+    auto ask_page = [&](int i) { return i < to ? page_of(p.b, t.seq, place(i).index) : 0; };
+    auto put_place = [&](int i, int page) {
         if (i >= to) return;
         // a page that the pool does not have is read as its first
         const int pg = (unsigned)page < (unsigned)p.c.pages ? page : 0, in = place(i).in;
@@ -449,8 +445,8 @@ __global__ __launch_bounds__(WAVES * 64, (DP > 128 ? 1 : 2)) void attend_tile_ke
     };
     auto look_up = [&](int i) {  // i: a block's first stage
         put_scales(i + WAVES + wave);
-        put_place(i + 2 * WAVES + wave);
-        ask_page(i + 3 * WAVES + wave);
+        put_place(i + 2 * WAVES + wave, page);
+        page = ask_page(i + 3 * WAVES + wave);
     };
     // A thread's pieces of K and of V: piece j of key key_of(j).
     constexpr bool EVEN = NT % PR == 0;
@@ -618,12 +614,11 @@ __global__ __launch_bounds__(WAVES * 64, (DP > 128 ? 1 : 2)) void attend_tile_ke
         if (i < to) store_v(i);
     };
     // the blocks before the first
-    ask_page(from + wave);
-    put_place(from + wave);
-    ask_page(from + WAVES + wave);
+    const int page0 = ask_page(from + wave), page1 = ask_page(from + WAVES + wave);
+    page = ask_page(from + 2 * WAVES + wave);
+    put_place(from + wave, page0);
     put_scales(from + wave);
-    put_place(from + WAVES + wave);
-    ask_page(from + 2 * WAVES + wave);
+    put_place(from + WAVES + wave, page1);
     __syncthreads();
     if (from < to) {
         load_rows(from, kbase, rk);
@@ -632,6 +627,8 @@ __global__ __launch_bounds__(WAVES * 64, (DP > 128 ? 1 : 2)) void attend_tile_ke
     }
     __syncthreads();
     const bool idle = w0 > most;  // no rows
+#pragma unroll
+    for (int s = 0; s < DS; ++s) q[s] = in_place(q[s]);  // waited for here, not in the loop
     for (int i = from; i < to; ++i) {
         if ((i - from) % WAVES == 0) look_up(i);
         if (!idle) {
@@ -675,7 +672,8 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendParams p) {
     constexpr int DS = NK * (Q8 ? 2 : 1);  // instructions of the first product
     constexpr int DO = DP / 16;
     constexpr int VLDS = KT * PITCH * 2, OLDS = ROWS * (DP + 4) * 4;
-    __shared__ __attribute__((aligned(16))) char s_mem[VLDS * WAVES > OLDS ? VLDS * WAVES : OLDS];
+    constexpr int SETS = OLDS * WAVES <= VLDS * WAVES + 4096 ? WAVES : 1;  // of the waves' sums at the end
+    __shared__ __attribute__((aligned(16))) char s_mem[VLDS * WAVES > OLDS * SETS ? VLDS * WAVES : OLDS * SETS];
     __shared__ float s_ml[WAVES][ROWS][2];
 
     const int head = blockIdx.x % p.c.heads;
@@ -865,7 +863,7 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendParams p) {
             s_ml[wave][g * 16 + col][1] = l[g];
         }
     }
-    __syncthreads();
+    __syncthreads();  // V in LDS is no longer needed either
     float* const s_o = reinterpret_cast<float*>(s_mem);
     float total[G], mx[G];
 #pragma unroll
@@ -877,20 +875,22 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendParams p) {
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) {
             const float mw = s_ml[w][g * 16 + col][0];
-            total[g] += mw == -INFINITY ? 0.0f * s_ml[w][g * 16 + col][1] : s_ml[w][g * 16 + col][1] * __builtin_amdgcn_exp2f(mw - mx[g]);
+            total[g] += mw == -INFINITY ? 0.0f : s_ml[w][g * 16 + col][1] * __builtin_amdgcn_exp2f(mw - mx[g]);
         }
         const float f = m[g] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[g] - mx[g]);
 #pragma unroll
         for (int d = 0; d < DO; ++d) o[g][d] *= f;
     }
-    for (int w = 0; w < WAVES; ++w) {
-        if (wave == w) {
+    // SETS of the waves' sums have room side by side; the waves beyond add to those
+#pragma unroll
+    for (int w0 = 0; w0 < WAVES; w0 += SETS) {
+        if (wave >= w0 && wave < w0 + SETS) {
 #pragma unroll
             for (int g = 0; g < G; ++g)
 #pragma unroll
                 for (int d = 0; d < DO; ++d) {
-                    floatx4* at = reinterpret_cast<floatx4*>(s_o + (g * 16 + col) * (DP + 4) + d * 16 + quad * 4);
-                    if (w == 0) *at = o[g][d];
+                    floatx4* at = reinterpret_cast<floatx4*>(s_o + (wave - w0) * OLDS / 4 + (g * 16 + col) * (DP + 4) + d * 16 + quad * 4);
+                    if (w0 == 0) *at = o[g][d];
                     else *at += o[g][d];
                 }
         }
@@ -898,12 +898,14 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendParams p) {
     }
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-        if (g % WAVES != wave && G >= WAVES) continue;
         const float inv = inverse<DT, Q8>(total[g]);
 #pragma unroll
         for (int d = 0; d < DO; ++d) {
-            if (G < WAVES && (g * DO + d) % WAVES != wave) continue;
-            const floatx4 v = *reinterpret_cast<const floatx4*>(s_o + (g * 16 + col) * (DP + 4) + d * 16 + quad * 4);
+            if ((g * DO + d) % WAVES != wave) continue;
+            floatx4 v = {};
+#pragma unroll
+            for (int w = 0; w < SETS; ++w)
+                v += *reinterpret_cast<const floatx4*>(s_o + w * OLDS / 4 + (g * 16 + col) * (DP + 4) + d * 16 + quad * 4);
             put4<DT>(p, row[g], part, d * 16 + quad * 4, v[0], v[1], v[2], v[3], inv);
         }
         if (wave == g % WAVES && quad == 0) put_weight(p, row[g], part, mx[g], total[g]);
@@ -911,29 +913,61 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendParams p) {
 }
 
 // --------------------------------------------------------------------- join --
-// A wave a row: the parts' sums, brought to their common maximum and added in
-// order.
-template <int DT, bool Q8>
+// W waves a row: the parts' sums, brought to their common maximum and added in
+// order, every wave's W-th part by itself first.  All of a row's maxima are read
+// at once, a part a lane.  (64 parts of 32 rows: 25 us read one after another, 4 so.)
+template <int DT, bool Q8, int W>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p) {
-    const int heads = p.c.heads * p.group;
+    static_assert(W == 1 || W == 4, "a workgroup has 4 waves");
+    __shared__ floatx4 s_o[W > 1 ? W : 1][64];
+    const int heads = p.c.heads * p.group, wave = wave_of(), lane = threadIdx.x & 63;
     const long long rows = (long long)p.b.tokens * heads;
-    const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const long long r = W > 1 ? (long long)blockIdx.x : (long long)blockIdx.x * 4 + wave;
     if (r >= rows) return;
-    const int lane = threadIdx.x & 63, token = (int)(r / heads), head = (int)(r - (long long)token * heads);
+    const int token = (int)(r / heads), head = (int)(r - (long long)token * heads);
     if (sequence_of(p.b, token) < 0) return;  // no row: nobody wrote its parts
-    float mx = -INFINITY;
-    for (int s = 0; s < p.parts; ++s) mx = fmaxf(mx, p.part_ml[2 * (s * rows + r)]);
-    floatx4 sum = {};
+    float m[2], l[2], mx = -INFINITY;  // parts lane and lane + 64
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int s = lane + 64 * i;
+        m[i] = -INFINITY, l[i] = 0.0f;
+        if (s < p.parts) m[i] = p.part_ml[2 * (s * rows + r)], l[i] = p.part_ml[2 * (s * rows + r) + 1];
+        mx = fmaxf(mx, m[i]);
+    }
+#pragma unroll
+    for (int o = 32; o; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
     float total = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        m[i] = m[i] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[i] - mx);  // sums of no key are zeros
+        total += l[i] * m[i];
+    }
+#pragma unroll
+    for (int o = 32; o; o >>= 1) total += __shfl_xor(total, o);
+    floatx4 sum = {};
     const bool on = lane * 4 < p.c.dim;
-#pragma unroll 4
-    for (int s = 0; s < p.parts; ++s) {
-        const float m = p.part_ml[2 * (s * rows + r)], l = p.part_ml[2 * (s * rows + r) + 1];
-        floatx4 v = {};
-        if (on) v = *reinterpret_cast<const floatx4*>(p.part_o + (s * rows + r) * p.c.dim + lane * 4);
-        const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - mx);  // sums of no key are zeros
-        total += l * f;
-        sum += v * f;
+    const float* const at = p.part_o + r * p.c.dim + lane * 4;
+    constexpr int U = 8;  // parts whose rows are on their way together
+    for (int s0 = W > 1 ? wave : 0; s0 < p.parts; s0 += U * W) {
+        floatx4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + u * W;
+            v[u] = floatx4{};
+            if (on && s < p.parts) v[u] = *reinterpret_cast<const floatx4*>(at + s * rows * p.c.dim);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + u * W;
+            sum += v[u] * __shfl(s < 64 ? m[0] : m[1], s & 63);
+        }
+    }
+    if constexpr (W > 1) {
+        s_o[wave][lane] = sum;
+        __syncthreads();
+        if (wave) return;
+#pragma unroll
+        for (int w = 1; w < W; ++w) sum += s_o[w][lane];
     }
     const float inv = inverse<DT, Q8>(total);
     if (!on) return;
@@ -959,12 +993,18 @@ void launch_dim(const AttendPlan& plan, const AttendParams& p, hipStream_t strea
 template <int DT, bool Q8>
 hipError_t launch_type(const AttendPlan& plan, const AttendParams& p, hipStream_t stream) {
     if (p.c.dim <= 64) launch_dim<DT, Q8, 64>(plan, p, stream);
+    else if (p.c.dim <= 96) launch_dim<DT, Q8, 96>(plan, p, stream);
     else if (p.c.dim <= 128) launch_dim<DT, Q8, 128>(plan, p, stream);
+    else if (p.c.dim <= 192) launch_dim<DT, Q8, 192>(plan, p, stream);
     else launch_dim<DT, Q8, 256>(plan, p, stream);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.parts <= 1) return e;
     const long long rows = (long long)p.b.tokens * p.c.heads * p.group;
-    attend_join_kernel<DT, Q8><<<dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream>>>(p);
+    // a wave a row where the parts are few, a workgroup where they are many
+    if (p.parts <= 8)
+        attend_join_kernel<DT, Q8, 1><<<dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream>>>(p);
+    else
+        attend_join_kernel<DT, Q8, 4><<<dim3((unsigned)rows), dim3(256), 0, stream>>>(p);
     return hipGetLastError();
 }
 

@@ -16,9 +16,9 @@ AttendPlan attend_plan(int tokens, int sequences, int heads, int group, int dim,
     // keys that a tile's rows see, at most
     const long long span = (plan.rows + group - 1) / group;
     const long long keys = std::min(max_len, (long long)window + sinks + span + 64);
-    const long long want = plan.form == ATT_TILE ? 256 : 768;  // workgroups that fill the device
-    const long long least = plan.form == ATT_TILE ? 512 : 256; // keys that are worth a part
-    long long parts = std::min((want + tiles - 1) / tiles, (keys + least - 1) / least);
+    const long long want = plan.form == ATT_TILE || dim > 128 ? 256 : 512;  // workgroups that fill the device
+    const long long least = plan.form == ATT_TILE ? 512 : 128; // keys that are worth a part
+    long long parts = std::min((want + tiles / 2) / tiles, (keys + least - 1) / least);
     plan.parts = (int)std::max(1LL, std::min(parts, 128LL));
     return plan;
 }
