@@ -1115,7 +1115,7 @@ def kv_write(cache: KVCache, k, v, lens, table=None, starts=None, stream=None) -
 
 def kv_read(cache: KVCache, tokens: int, lens, table=None, starts=None, dtype=None, k=None, v=None, stream=None):
     """The last tokens of every sequence out of the cache: (k, v), each
-    [tokens, heads, dim] of dtype (the cache's own, or bf16 from 8 bits, by default).
+    [tokens, heads, dim] of dtype (by default the cache's, or bf16 from 8 bits).
     tokens counts them all; lens, table and starts as for kv_write.  Rows of
     tokens that belong to no sequence are left as they are (k and v may name
     the tensors to write)."""

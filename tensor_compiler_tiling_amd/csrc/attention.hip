@@ -391,11 +391,9 @@ __global__ __launch_bounds__(WAVES * 64, (DP > 128 ? 1 : 2)) void attend_tile_ke
     const Keys keys = keys_of<KT>(p, t, t.r0, ROWS);
     int from, to;
     part_of(p, keys.total(), part, from, to);
-    // tokens of the wave's rows, and the keys that they can see
+    // tokens of the wave's rows, and of the workgroup's
     const int most = t.count * p.group - 1, w0 = t.r0 + wave * 32;
     const int i0 = scalar(w0 / p.group), i1 = scalar((w0 + 31 < most ? w0 + 31 : most) / p.group);
-    const int wave_hi = w0 > most ? 0 : p.tree ? t.len : t.ctx + i1 + 1;
-    const int wave_lo = p.tree ? 0 : t.ctx + i0 - p.window + 1;
     const int a0 = scalar(t.r0 / p.group), a1 = scalar((t.r0 + ROWS - 1 < most ? t.r0 + ROWS - 1 : most) / p.group);
 
     uint4v q[DS];
@@ -921,10 +919,10 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p) {
     static_assert(W == 1 || W == 4, "a workgroup has 4 waves");
     __shared__ floatx4 s_o[W > 1 ? W : 1][64];
     const int heads = p.c.heads * p.group, wave = wave_of(), lane = threadIdx.x & 63;
-    const long long rows = (long long)p.b.tokens * heads;
-    const long long r = W > 1 ? (long long)blockIdx.x : (long long)blockIdx.x * 4 + wave;
+    const long long rows = p.b.tokens * heads;  // below 2^26
+    const int r = W > 1 ? (int)blockIdx.x : (int)blockIdx.x * 4 + wave;
     if (r >= rows) return;
-    const int token = (int)(r / heads), head = (int)(r - (long long)token * heads);
+    const int token = r / heads, head = r - token * heads;
     if (sequence_of(p.b, token) < 0) return;  // no row: nobody wrote its parts
     float m[2], l[2], mx = -INFINITY;  // parts lane and lane + 64
 #pragma unroll
@@ -946,7 +944,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p) {
     for (int o = 32; o; o >>= 1) total += __shfl_xor(total, o);
     floatx4 sum = {};
     const bool on = lane * 4 < p.c.dim;
-    const float* const at = p.part_o + r * p.c.dim + lane * 4;
+    const float* const at = p.part_o + (long long)r * p.c.dim + lane * 4;
     constexpr int U = 8;  // parts whose rows are on their way together
     for (int s0 = W > 1 ? wave : 0; s0 < p.parts; s0 += U * W) {
         floatx4 v[U];

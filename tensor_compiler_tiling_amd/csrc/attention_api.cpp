@@ -107,6 +107,8 @@ int check_batch(const ct_kv_batch* b, const KvPages& c, KvBatch* out) {
     if ((long long)o.width * c.page > kMaxPlaces) return fail(CT_ERR_UNSUPPORTED, "more than 2^30 places a sequence");
     if ((long long)b->tokens * c.heads > kMaxRows) return fail(CT_ERR_UNSUPPORTED, "2^26 rows or more in a call");
     if (b->sequences > 1 << 24) return fail(CT_ERR_UNSUPPORTED, "more than 2^24 sequences");
+    // attention's workgroups count through the starts
+    if (b->starts && b->sequences > 1 << 16) return fail(CT_ERR_UNSUPPORTED, "more than 2^16 sequences with starts");
     o.lens = b->lens, o.starts = b->starts, o.table = b->table;
     o.ldt = b->sequences > 1 ? b->ldt : 0;
     o.tokens = b->tokens, o.sequences = b->sequences;
@@ -136,6 +138,7 @@ int rows_call(const ct_kv_cache* cache, const ct_kv_batch* batch, const void* k,
     if (n == 0) return CT_OK;
     st = check_rows("k", k, k_token, k_head, n, p.c.heads, p.c.dim, dtype, !write);
     if (st == CT_OK) st = check_rows("v", v, v_token, v_head, n, p.c.heads, p.c.dim, dtype, !write);
+    if (st == CT_OK && write && cache->k == cache->v) return fail(CT_ERR_INVALID_ARG, "cache: k and v must not be the same");
     if (st == CT_OK && !write && k == v) return fail(CT_ERR_INVALID_ARG, "k and v must not be the same");
     if (st == CT_OK && (k == cache->k || k == cache->v || v == cache->k || v == cache->v))
         return fail(CT_ERR_INVALID_ARG, "k and v must not be the cache's own");

@@ -19,7 +19,10 @@
 //
 // Bound by memory.  LPR lanes hold a row, 8 elements each, and a group of them
 // does a token's key and its value, so that two loads are in flight and the
-// place is looked up once.
+// place is looked up once.  Measured: 32768 tokens of 8 heads of 128 from bf16 to
+// e4m3 49 us (203 MB, 4.1 TB/s; 52 with a token's heads in a workgroup, whose
+// scales' lines several then write), back 46 us (4.4 TB/s); 2 and 4 tokens a group
+// of lanes 50 and 58 us; a step of 48 tokens 3.9 us.
 #include "kv_device.hpp"
 
 namespace ct {
@@ -122,8 +125,9 @@ __global__ __launch_bounds__(kThreads) void kv_rows_kernel(KvRowsParams p) {
     constexpr int RPB = kThreads / LPR;
     constexpr int ES = DT == DT_F32 ? 4 : 2, CS = CDT == DT_E4M3 ? 1 : 2;
     const int lane = threadIdx.x % LPR;
-    const long long r = (long long)blockIdx.x * RPB + threadIdx.x / LPR;
-    const int token = (int)(r / p.c.heads), head = (int)(r - (long long)token * p.c.heads);
+    // a workgroup has neighbouring tokens of one head: whole lines of the cache and of its scales
+    const int block = blockIdx.x / p.c.heads, head = blockIdx.x - block * p.c.heads;
+    const int token = block * RPB + (int)threadIdx.x / LPR;
     // the lanes of a row go together; those past its elements help in its maximum
     const bool on = token < p.b.tokens && lane * kV < p.c.dim;
     char* const k = p.k + token * p.k_token + head * p.k_head + lane * kV * ES;
@@ -172,8 +176,8 @@ template <int CDT, int DT, bool WRITE>
 hipError_t launch_lanes(const KvRowsParams& p, hipStream_t stream) {
     auto go = [&](auto lanes) {
         constexpr int LPR = decltype(lanes)::value, RPB = kThreads / LPR;
-        const long long rows = (long long)p.b.tokens * p.c.heads;
-        kv_rows_kernel<CDT, DT, LPR, WRITE><<<dim3((unsigned)((rows + RPB - 1) / RPB)), dim3(kThreads), 0, stream>>>(p);
+        const dim3 blocks((unsigned)((p.b.tokens + RPB - 1) / RPB * p.c.heads));
+        kv_rows_kernel<CDT, DT, LPR, WRITE><<<blocks, dim3(kThreads), 0, stream>>>(p);
         return hipGetLastError();
     };
     if (p.c.dim <= 64) return go(std::integral_constant<int, 8>{});

@@ -91,6 +91,7 @@ def test_batches_beyond_the_kernels(call):
     assert CALLS[call](batch=dict(BATCH, tokens=1 << 25)) == ct.CT_ERR_UNSUPPORTED
     assert CALLS[call](batch=dict(BATCH, width=1 << 27, ldt=1 << 27)) == ct.CT_ERR_UNSUPPORTED
     assert CALLS[call](batch=dict(BATCH, starts=P, sequences=(1 << 24) + 1)) == ct.CT_ERR_UNSUPPORTED
+    assert CALLS[call](batch=dict(BATCH, starts=P, sequences=(1 << 16) + 1)) == ct.CT_ERR_UNSUPPORTED
 
 
 @pytest.mark.parametrize("call", list(CALLS))
@@ -112,6 +113,10 @@ def test_null_structs_and_no_tokens(call):
 def test_rows_that_are_refused(read, bad):
     assert write(read=read, **bad) == ct.CT_ERR_INVALID_ARG
     assert ct.ct_last_error()
+
+
+def test_one_place_for_keys_and_values_is_not_written():
+    assert write(dict(CACHE, v=P)) == ct.CT_ERR_INVALID_ARG and "must not be the same" in ct.ct_last_error()
 
 
 def test_rows_read_to_one_place_are_refused():
