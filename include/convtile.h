@@ -568,10 +568,11 @@ int ct_kv_attention_fwd(const ct_kv_cache* cache, const ct_kv_batch* batch, cons
                         long long max_len, void* workspace, long long workspace_bytes,
                         void* stream);
 
-/* Bytes of workspace that a call of these sizes needs (window 0: none); < 0 (a
- * status) for sizes that it refuses.  Host only. */
+/* Bytes of workspace that a call of these sizes over a cache of cache_dtype
+ * needs (window 0: none); < 0 (a status) for what it refuses.  Host only. */
 long long ct_kv_attention_workspace_bytes(int tokens, int sequences, int heads, int kv_heads,
-                                          int dim, long long max_len, int window, int sinks);
+                                          int dim, long long max_len, int window, int sinks,
+                                          int cache_dtype);
 
 /* ---- tile-config search ----------------------------------------------
  * The space of a shape follows the TVM tutorial's template (Step 1): ordered

@@ -171,7 +171,7 @@ _SIGS = {
     "ct_kv_write": (_I, [_P, _P, _P, _LL, _LL, _P, _LL, _LL, _I, _P]),
     "ct_kv_read": (_I, [_P, _P, _P, _LL, _LL, _P, _LL, _LL, _I, _P]),
     "ct_kv_attention_fwd": (_I, [_P, _P, _P, _P, _LL, _LL, _P, _LL, _LL, _I, _I, _F, _LL, _P, _LL, _P]),
-    "ct_kv_attention_workspace_bytes": (_LL, [_I] * 5 + [_LL, _I, _I]),
+    "ct_kv_attention_workspace_bytes": (_LL, [_I] * 5 + [_LL, _I, _I, _I]),
     "ct_variant_count": (_I, []),
     "ct_variant_info": (_I, [_I, ctypes.POINTER(ct_variant_desc)]),
     "ct_split_count": (_LL, [_LL, _I]),
@@ -440,9 +440,11 @@ def ct_kv_attention_fwd(cache, batch, mask, q, q_token, q_head, y, y_token, y_he
                                        workspace_bytes, _stream(stream))
 
 
-def ct_kv_attention_workspace_bytes(tokens, sequences, heads, kv_heads, dim, max_len=0, window=0, sinks=0) -> int:
+def ct_kv_attention_workspace_bytes(tokens, sequences, heads, kv_heads, dim, max_len=0, window=0, sinks=0,
+                                    cache_dtype=CT_BF16) -> int:
     _counts(tokens=tokens, sequences=sequences, heads=heads, kv_heads=kv_heads, dim=dim, window=window, sinks=sinks)
-    return _load().ct_kv_attention_workspace_bytes(tokens, sequences, heads, kv_heads, dim, max_len, window, sinks)
+    return _load().ct_kv_attention_workspace_bytes(tokens, sequences, heads, kv_heads, dim, max_len, window, sinks,
+                                                   cache_dtype)
 
 
 def ct_linear_workspace_bytes(M, N, K, dtype) -> int:
@@ -1197,7 +1199,7 @@ def kv_attention(q, cache: KVCache, lens, table=None, starts=None, max_len=None,
     yt, yh = _heads("out", out, index, dtype, shape)
     reach = (b.width if table is not None else 1) * cache.page
     longest = reach if max_len is None else max(1, min(max_len, reach))
-    need = _attention_bytes(tokens, b.sequences, heads, cache.heads, dim, longest, window, sinks)
+    need = _attention_bytes(tokens, b.sequences, heads, cache.heads, dim, longest, window, sinks, cache._c.dtype)
     sp = None
     if need:
         space = T.empty((need,), (1,), dtype=T.uint8, device=cache.device)

@@ -115,6 +115,12 @@ __device__ __forceinline__ T in_place(T v) {
     return v;
 }
 
+// What sums at maximum m are scaled by for a greater one: at least the least
+// normal number, so that what is infinite stays so.
+__device__ __forceinline__ float fall_to(float m, float next) {
+    return m == -INFINITY ? 1.0f : fmaxf(__builtin_amdgcn_exp2f(m - next), 0x1p-126f);
+}
+
 // The greater of a lane's value and that of the lane 32 away.
 __device__ __forceinline__ float max_of_halves(float v) {
     typedef unsigned int pair __attribute__((ext_vector_type(2)));
@@ -367,6 +373,17 @@ __device__ __forceinline__ void part_of(const AttendParams& p, int total, int pa
 // where 8-bit rows widen), two stages' room.  Rows of K in LDS are 16 bytes longer
 // than dim: 16 neighbouring keys, read 16 bytes each, then cover all 64 banks.  Those
 // of V lie 64 bytes (mod 256) apart: a transposing read takes 64 bytes of 8 keys.
+//
+// Measured: a prompt of 8192 tokens, 32 heads on 8, dim 128 bf16 572 us (550 GFLOP,
+// 962 TFLOP/s; a library product of 8192^3 reaches 1227), matrix units 44% busy at
+// the 1.9 GHz that the chip holds.  What bounds it is the products themselves at
+// that clock: without the exponentials a copy took 539 us, without any weights
+// 521, without reading LDS 541.  Long 16-bit caches of single tokens run at
+// 5.1 TB/s.  Other forms of it took, for that prompt: two halves of the waves that
+// take turns at products and weights, with two barriers a turn, 606 to 651 us; the
+// second product's instructions between the exponentials 643 (a wave that waits for
+// the matrix unit holds its own other work up); stages of 32 keys 890, workgroups of
+// 4 waves 887 (against 747 then); more priority for the products 617.
 template <int DT, bool Q8, int DP, int WAVES, int KT>
 __global__ __launch_bounds__(WAVES * 64, (DP > 128 ? 1 : 2)) void attend_tile_kernel(AttendParams p) {
     constexpr int NT = WAVES * 64, ROWS = WAVES * 32, NK = KT / 32;
@@ -562,8 +579,7 @@ __global__ __launch_bounds__(WAVES * 64, (DP > 128 ? 1 : 2)) void attend_tile_ke
         top = max_of_halves(top) * p.scale;
         if (__any(top > m + kLag)) {
             const float next = fmaxf(m, top);
-            // at least the least normal number: what is infinite stays so
-            const float fall = m == -INFINITY ? 1.0f : fmaxf(__builtin_amdgcn_exp2f(m - next), 0x1p-126f);
+            const float fall = fall_to(m, next);
             l *= fall;
 #pragma unroll
             for (int d = 0; d < DO; ++d)
@@ -657,12 +673,16 @@ __global__ __launch_bounds__(WAVES * 64, (DP > 128 ? 1 : 2)) void attend_tile_ke
 }
 
 // --------------------------------------------------------------- row kernel --
-// Up to 16 G rows.  Memory bounds it, so a wave keeps its own keys: 32 at a time,
+// Up to 16 rows.  Memory bounds it, so a wave keeps its own keys: 32 at a time,
 // K straight to the registers of the first product, V through the wave's own
-// piece of LDS; no barrier until the waves' sums are joined.
-template <int DT, bool Q8, int DP, int G>
+// piece of LDS; no barrier until the waves' sums are joined.  Two workgroups a CU
+// are enough: registers for three or four (__launch_bounds__) took 64 sequences of
+// up to 8192 tokens in e4m3 from 161 to 176 and 206 us.  Measured: that 157 us
+// (723 MB, 4.6 TB/s), 100 windows of 1024 fp16 28 (106 MB), one token of 1200
+// bf16 12 with the join, a chain of five reads that wait for each other.
+template <int DT, bool Q8, int DP>
 __global__ __launch_bounds__(256) void attend_rows_kernel(AttendParams p) {
-    constexpr int WAVES = 4, KT = 32, ROWS = 16 * G;
+    constexpr int WAVES = 4, KT = 32, ROWS = 16;
     constexpr int PITCH = DP + 16;         // of V in LDS: a transposing read takes 32 bytes of 16 keys
     constexpr int PIECE = Q8 ? 16 : 8;
     constexpr int PR = DP / PIECE;
@@ -687,26 +707,18 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendParams p) {
     const int most = t.count * p.group - 1;
     const int i0 = t.r0 / p.group, i1 = (t.r0 + ROWS - 1 < most ? t.r0 + ROWS - 1 : most) / p.group;
 
-    Row row[G];
-    uint4v q[G][DS];
+    const Row row = row_of(p, t, head * p.group, t.r0 + col);
+    uint4v q[DS];
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-        row[g] = row_of(p, t, head * p.group, t.r0 + g * 16 + col);
-#pragma unroll
-        for (int s = 0; s < DS; ++s) {
-            q[g][s] = uint4v{0, 0, 0, 0};
-            const int d = Q8 ? 16 * (4 * (s / 2) + quad) + 8 * (s % 2) : 8 * (4 * s + quad);
-            if (row[g].token >= 0 && d < p.c.dim) q[g][s] = load16(p.q + row[g].token * p.q_token + row[g].head * p.q_head + d * 2);
-        }
+    for (int s = 0; s < DS; ++s) {
+        q[s] = uint4v{0, 0, 0, 0};
+        const int d = Q8 ? 16 * (4 * (s / 2) + quad) + 8 * (s % 2) : 8 * (4 * s + quad);
+        if (row.token >= 0 && d < p.c.dim) q[s] = load16(p.q + row.token * p.q_token + row.head * p.q_head + d * 2);
     }
-    floatx4 o[G][DO];
-    float m[G], l[G];
+    floatx4 o[DO];
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-#pragma unroll
-        for (int d = 0; d < DO; ++d) o[g][d] = floatx4{};
-        m[g] = -INFINITY, l[g] = 0.0f;
-    }
+    for (int d = 0; d < DO; ++d) o[d] = floatx4{};
+    float m = -INFINITY, l = 0.0f;
 
     const char* const kbase = p.c.k + head * p.c.ld_head;
     const char* const vbase = p.c.v + head * p.c.ld_head;
@@ -771,58 +783,53 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendParams p) {
                     *reinterpret_cast<uint4v*>(s_v + k * PITCH + (4 * j + quad) * PIECE + 8 * e) = v;
                 }
             }
-        floatx4 z[G][2];
-#pragma unroll
-        for (int g = 0; g < G; ++g) z[g][0] = z[g][1] = floatx4{};
+        floatx4 z[2];
+z[0] = z[1] = floatx4{};
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int s = 0; s < DS; ++s) {
                 const uint4v a = Q8 ? widen8<DT>(rk[h][s / 2], s % 2, sk[h]) : rk[h][s];
-#pragma unroll
-                for (int g = 0; g < G; ++g) z[g][h] = mma16<DT>(a, q[g][s], z[g][h]);
+z[h] = mma16<DT>(a, q[s], z[h]);
             }
         if (i + WAVES < to) {
             load_rows(i + WAVES);
             if (i + 2 * WAVES < to) load_pages(i + 2 * WAVES);
         }
-        uint4v w[G];
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            if (!whole) {
-                const unsigned bits = (unsigned)seen(p, t, row[g], k0) >> (4 * quad);
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (!(bits >> (h * 16 + e) & 1)) z[g][h][e] = -INFINITY;
-            }
-            float top = -INFINITY;
+        uint4v w;
+        if (!whole) {
+            const unsigned bits = (unsigned)seen(p, t, row, k0) >> (4 * quad);
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) top = fmaxf(top, z[g][h][e]);
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32)) * p.scale;
-            if (__any(top > m[g] + kLag)) {
-                const float next = fmaxf(m[g], top);
-                const float f = m[g] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[g] - next);
-                l[g] *= f;
+                for (int e = 0; e < 4; ++e)
+                    if (!(bits >> (h * 16 + e) & 1)) z[h][e] = -INFINITY;
+        }
+        float top = -INFINITY;
 #pragma unroll
-                for (int d = 0; d < DO; ++d) o[g][d] *= f;
-                m[g] = next;
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, z[h][e]);
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32)) * p.scale;
+        if (__any(top > m + kLag)) {
+            const float next = fmaxf(m, top);
+            const float fall = fall_to(m, next);
+            l *= fall;
+#pragma unroll
+            for (int d = 0; d < DO; ++d) o[d] *= fall;
+            m = next;
+        }
+        const float base = m == -INFINITY ? 0.0f : m - p_shift<DT>();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                z[h][e] = __builtin_amdgcn_exp2f(fmaf(z[h][e], p.scale, -base));
+                l += z[h][e];
             }
-            const float base = m[g] == -INFINITY ? 0.0f : m[g] - p_shift<DT>();
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    z[g][h][e] = __builtin_amdgcn_exp2f(fmaf(z[g][h][e], p.scale, -base));
-                    l[g] += z[g][h][e];
-                }
-                w[g][2 * h] = pack2<DT>(z[g][h][0], z[g][h][1]);
-                w[g][2 * h + 1] = pack2<DT>(z[g][h][2], z[g][h][3]);
-            }
+            w[2 * h] = pack2<DT>(z[h][0], z[h][1]);
+            w[2 * h + 1] = pack2<DT>(z[h][2], z[h][3]);
         }
         wave_fence();  // V is read by other lanes than those that wrote it
         const uint16_t* vrow = s_v + (4 * quad + col / 4) * PITCH + 4 * (col & 3);
@@ -830,8 +837,7 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendParams p) {
         for (int d = 0; d < DO; ++d) {
             const uint2v a = read_transposed(vrow + d * 16), b = read_transposed(vrow + 16 * PITCH + d * 16);
             const uint4v v = {a[0], a[1], b[0], b[1]};
-#pragma unroll
-            for (int g = 0; g < G; ++g) o[g][d] = mma16<DT>(v, w[g], o[g][d]);
+            o[d] = mma16<DT>(v, w, o[d]);
         }
         wave_fence();  // and written anew once they have
         if (__any(bad)) {
@@ -839,75 +845,59 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendParams p) {
             for (int k = 0; k < KT; ++k) {
                 if (!__any(bad >> k & 1)) continue;
                 const CacheRow<DT, Q8> v(p, t, head, k0 + k);
+                if (!(seen(p, t, row, k0) >> k & 1)) continue;
+                const int d0 = in_place(4 * quad);
 #pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    if (!(seen(p, t, row[g], k0) >> k & 1)) continue;
-                    const int d0 = in_place(4 * quad);
+                for (int d = 0; d < DO; ++d)
 #pragma unroll
-                    for (int d = 0; d < DO; ++d)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[g][d][e] = in_place(o[g][d][e] + v.not_finite(d0 + d * 16 + e));
-                }
+                    for (int e = 0; e < 4; ++e) o[d][e] = in_place(o[d][e] + v.not_finite(d0 + d * 16 + e));
             }
         }
     }
     // the waves' sums, brought to their common maximum and added in order
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-        l[g] += __shfl_xor(l[g], 16);
-        l[g] += __shfl_xor(l[g], 32);
-        if (quad == 0) {
-            s_ml[wave][g * 16 + col][0] = m[g];
-            s_ml[wave][g * 16 + col][1] = l[g];
-        }
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    if (quad == 0) {
+        s_ml[wave][col][0] = m;
+        s_ml[wave][col][1] = l;
     }
     __syncthreads();  // V in LDS is no longer needed either
     float* const s_o = reinterpret_cast<float*>(s_mem);
-    float total[G], mx[G];
+    float total = 0.0f, mx = -INFINITY;
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-        mx[g] = -INFINITY;
+    for (int w = 0; w < WAVES; ++w) mx = fmaxf(mx, s_ml[w][col][0]);
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) mx[g] = fmaxf(mx[g], s_ml[w][g * 16 + col][0]);
-        total[g] = 0.0f;
-#pragma unroll
-        for (int w = 0; w < WAVES; ++w) {
-            const float mw = s_ml[w][g * 16 + col][0];
-            total[g] += mw == -INFINITY ? 0.0f : s_ml[w][g * 16 + col][1] * __builtin_amdgcn_exp2f(mw - mx[g]);
-        }
-        const float f = m[g] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[g] - mx[g]);
-#pragma unroll
-        for (int d = 0; d < DO; ++d) o[g][d] *= f;
+    for (int w = 0; w < WAVES; ++w) {
+        const float mw = s_ml[w][col][0];
+        total += mw == -INFINITY ? 0.0f : s_ml[w][col][1] * __builtin_amdgcn_exp2f(mw - mx);
     }
+    const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - mx);
+#pragma unroll
+    for (int d = 0; d < DO; ++d) o[d] *= f;
     // SETS of the waves' sums have room side by side; the waves beyond add to those
 #pragma unroll
     for (int w0 = 0; w0 < WAVES; w0 += SETS) {
         if (wave >= w0 && wave < w0 + SETS) {
 #pragma unroll
-            for (int g = 0; g < G; ++g)
-#pragma unroll
-                for (int d = 0; d < DO; ++d) {
-                    floatx4* at = reinterpret_cast<floatx4*>(s_o + (wave - w0) * OLDS / 4 + (g * 16 + col) * (DP + 4) + d * 16 + quad * 4);
-                    if (w0 == 0) *at = o[g][d];
-                    else *at += o[g][d];
-                }
+            for (int d = 0; d < DO; ++d) {
+                floatx4* at = reinterpret_cast<floatx4*>(s_o + (wave - w0) * OLDS / 4 + col * (DP + 4) + d * 16 + quad * 4);
+                if (w0 == 0) *at = o[d];
+                else *at += o[d];
+            }
         }
         __syncthreads();
     }
+    const float inv = inverse<DT, Q8>(total);
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-        const float inv = inverse<DT, Q8>(total[g]);
+    for (int d = 0; d < DO; ++d) {
+        if (d % WAVES != wave) continue;
+        floatx4 v = {};
 #pragma unroll
-        for (int d = 0; d < DO; ++d) {
-            if ((g * DO + d) % WAVES != wave) continue;
-            floatx4 v = {};
-#pragma unroll
-            for (int w = 0; w < SETS; ++w)
-                v += *reinterpret_cast<const floatx4*>(s_o + w * OLDS / 4 + (g * 16 + col) * (DP + 4) + d * 16 + quad * 4);
-            put4<DT>(p, row[g], part, d * 16 + quad * 4, v[0], v[1], v[2], v[3], inv);
-        }
-        if (wave == g % WAVES && quad == 0) put_weight(p, row[g], part, mx[g], total[g]);
+        for (int w = 0; w < SETS; ++w)
+            v += *reinterpret_cast<const floatx4*>(s_o + w * OLDS / 4 + col * (DP + 4) + d * 16 + quad * 4);
+        put4<DT>(p, row, part, d * 16 + quad * 4, v[0], v[1], v[2], v[3], inv);
     }
+    if (wave == 0 && quad == 0) put_weight(p, row, part, mx, total);
 }
 
 // --------------------------------------------------------------------- join --
@@ -980,12 +970,8 @@ void launch_dim(const AttendPlan& plan, const AttendParams& p, hipStream_t strea
     constexpr int WAVES = DP > 128 ? 4 : 8;
     if (plan.form == ATT_TILE)
         attend_tile_kernel<DT, Q8, DP, WAVES, 64><<<grid, dim3(WAVES * 64), 0, stream>>>(p);
-    else if (plan.form == ATT_ROW16)
-        attend_rows_kernel<DT, Q8, DP, 1><<<grid, dim3(256), 0, stream>>>(p);
-    else if (plan.form == ATT_ROW32 || DP > 128)
-        attend_rows_kernel<DT, Q8, DP, 2><<<grid, dim3(256), 0, stream>>>(p);
     else
-        attend_rows_kernel<DT, Q8, DP, (DP > 128 ? 2 : 4)><<<grid, dim3(256), 0, stream>>>(p);
+        attend_rows_kernel<DT, Q8, DP><<<grid, dim3(256), 0, stream>>>(p);
 }
 
 template <int DT, bool Q8>

@@ -154,10 +154,12 @@ int rows_call(const ct_kv_cache* cache, const ct_kv_batch* batch, const void* k,
 
 // The sizes of a call, whose plan goes to `plan` (not for no tokens).
 int check_sizes(int tokens, int sequences, int heads, int kv_heads, int dim, long long max_len, int window, int sinks,
-                AttendPlan* plan) {
+                int cache_dtype, AttendPlan* plan) {
     if (tokens < 0 || sequences < 0 || heads < 1 || kv_heads < 1 || dim < 1 || max_len < 0)
         return fail(CT_ERR_INVALID_ARG, "counts must not be negative, heads and dim must be positive");
     if (heads % kv_heads) return fail(CT_ERR_INVALID_ARG, "%d heads of q for %d of the cache", heads, kv_heads);
+    if (cache_dtype != CT_F16 && cache_dtype != CT_BF16 && cache_dtype != CT_E4M3)
+        return fail(CT_ERR_INVALID_ARG, "cache: unknown dtype %d", cache_dtype);
     if (window < 0 || sinks < 0) return fail(CT_ERR_INVALID_ARG, "window and sinks must not be negative");
     if (sinks && !window) return fail(CT_ERR_INVALID_ARG, "sinks belong to a window");
     if (dim % 16 || dim > 256) return fail(CT_ERR_UNSUPPORTED, "rows of %d elements (whole multiples of 16 up to 256)", dim);
@@ -166,7 +168,8 @@ int check_sizes(int tokens, int sequences, int heads, int kv_heads, int dim, lon
     if (tokens == 0) return CT_OK;
     if (sequences < 1) return fail(CT_ERR_INVALID_ARG, "%d tokens of no sequence", tokens);
     const long long most = max_len && max_len < kMaxPlaces ? max_len : kMaxPlaces;
-    *plan = attend_plan(tokens, sequences, kv_heads, heads / kv_heads, dim, most, window ? window : kNoWindow, sinks);
+    *plan = attend_plan(tokens, sequences, kv_heads, heads / kv_heads, dim, most, window ? window : kNoWindow, sinks,
+                        cache_dtype == CT_E4M3);
     return CT_OK;
 }
 
@@ -197,7 +200,7 @@ int ct_kv_attention_fwd(const ct_kv_cache* cache, const ct_kv_batch* batch, cons
     const ct_kv_mask& mk = mask ? *mask : none;
     const int n = batch->tokens;
     AttendPlan plan{};
-    st = check_sizes(n, batch->sequences, heads, cache->heads, cache->dim, max_len, mk.window, mk.sinks, &plan);
+    st = check_sizes(n, batch->sequences, heads, cache->heads, cache->dim, max_len, mk.window, mk.sinks, cache->dtype, &plan);
     if (st != CT_OK) return st;
     if (dtype != CT_F16 && dtype != CT_BF16) return fail(CT_ERR_INVALID_ARG, "q must be CT_F16 or CT_BF16, got %d", dtype);
     if (cache->dtype != CT_E4M3 && cache->dtype != dtype)
@@ -244,9 +247,9 @@ int ct_kv_attention_fwd(const ct_kv_cache* cache, const ct_kv_batch* batch, cons
 }
 
 long long ct_kv_attention_workspace_bytes(int tokens, int sequences, int heads, int kv_heads, int dim, long long max_len,
-                                          int window, int sinks) {
+                                          int window, int sinks, int cache_dtype) {
     ct::AttendPlan plan{};
-    const int st = ct::check_sizes(tokens, sequences, heads, kv_heads, dim, max_len, window, sinks, &plan);
+    const int st = ct::check_sizes(tokens, sequences, heads, kv_heads, dim, max_len, window, sinks, cache_dtype, &plan);
     if (st != CT_OK) return st;
     return tokens == 0 ? 0 : ct::attend_workspace_bytes(plan, tokens, heads, dim);
 }

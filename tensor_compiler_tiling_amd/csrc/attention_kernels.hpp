@@ -77,10 +77,8 @@ constexpr int kNoWindow = 1 << 30;  // past every distance
 
 // The kernel that attends.
 enum AttendForm {
-    ATT_ROW16 = 0,  // up to 16 rows (tokens x heads of a group) a tile, a wave's keys its own
-    ATT_ROW32 = 1,
-    ATT_ROW64 = 2,
-    ATT_TILE = 3,   // 32 rows a wave, the workgroup's keys shared through LDS
+    ATT_ROWS = 0,  // up to 16 rows (tokens x heads of a group) a tile, a wave's keys its own
+    ATT_TILE = 1,  // 32 rows a wave, the workgroup's keys shared through LDS
 };
 
 struct AttendPlan {
@@ -91,10 +89,10 @@ struct AttendPlan {
 
 // Rows of a form's tile.
 inline int attend_rows(int form, int dim) {
-    return form == ATT_ROW16 ? 16 : form == ATT_ROW32 ? 32 : form == ATT_ROW64 ? 64 : dim > 128 ? 128 : 256;
+    return form == ATT_ROWS ? 16 : dim > 128 ? 128 : 256;
 }
 
-AttendPlan attend_plan(int tokens, int sequences, int heads, int group, int dim, long long max_len, int window, int sinks);
+AttendPlan attend_plan(int tokens, int sequences, int heads, int group, int dim, long long max_len, int window, int sinks, bool q8);
 // Tiles of rows to launch.
 long long attend_tiles(const AttendPlan& plan, const KvBatch& b, int group);
 long long attend_workspace_bytes(const AttendPlan& plan, int tokens, int heads, int dim);

@@ -102,8 +102,8 @@ void refusals() {
     CHECK(attend(c, y, nullptr, 4, 1.0f, 0, 0) == CT_ERR_UNSUPPORTED);
     y = batch_of(0, 0, 0);
     CHECK(attend(c, y, nullptr, 4, 1.0f, 0, 0) == CT_OK);
-    CHECK(ct_kv_attention_workspace_bytes(INT_MAX, INT_MAX, INT_MAX, 1, 256, LLONG_MAX, INT_MAX, INT_MAX) == CT_ERR_UNSUPPORTED);
-    CHECK(ct_kv_attention_workspace_bytes(INT_MIN, 1, 1, 1, 16, 0, 0, 0) == CT_ERR_INVALID_ARG);
+    CHECK(ct_kv_attention_workspace_bytes(INT_MAX, INT_MAX, INT_MAX, 1, 256, LLONG_MAX, INT_MAX, INT_MAX, CT_F16) == CT_ERR_UNSUPPORTED);
+    CHECK(ct_kv_attention_workspace_bytes(INT_MIN, 1, 1, 1, 16, 0, 0, 0, CT_F16) == CT_ERR_INVALID_ARG);
 }
 
 void division() {
@@ -131,10 +131,9 @@ void plans() {
                         for (long long len : {1LL, 100LL, 5000LL, 131072LL, 1LL << 30})
                             for (int window : {ct::kNoWindow, 1, 1024}) {
                                 if ((long long)tokens * heads * group >= 1 << 26) continue;
-                                const ct::AttendPlan p = ct::attend_plan(tokens, sequences, heads, group, dim, len, window, 4);
+                                const ct::AttendPlan p = ct::attend_plan(tokens, sequences, heads, group, dim, len, window, 4, tokens % 2 == 0);
                                 CHECK(p.parts >= 1 && p.parts <= 128);
-                                CHECK(p.form >= ct::ATT_ROW16 && p.form <= ct::ATT_TILE);
-                                CHECK(p.form != ct::ATT_ROW64 || dim <= 128);
+                                CHECK(p.form == ct::ATT_ROWS || p.form == ct::ATT_TILE);
                                 CHECK(p.rows == ct::attend_rows(p.form, dim));
                                 const long long space = ct::attend_workspace_bytes(p, tokens, heads * group, dim);
                                 CHECK(space == (p.parts > 1 ? (long long)p.parts * tokens * heads * group * (dim + 2) * 4 : 0));

@@ -163,6 +163,7 @@ def test_workspace_bytes():
         assert f(*bad) == ct.CT_ERR_INVALID_ARG, bad
     for big in ((1, 1, 8, 2, 120), (1, 1, 8, 2, 272), (1 << 26, 1, 8, 2, 128), (1 << 25, 1 << 25, 1, 1, 128), (1, 1, 1 << 17, 1, 128)):
         assert f(*big) == ct.CT_ERR_UNSUPPORTED, big
+    assert f(1, 1, 8, 2, 128, 64, 0, 0, ct.CT_F32) == ct.CT_ERR_INVALID_ARG
     # a window bounds what there is to share
     assert f(1, 1, 8, 8, 128, 1 << 20, 128, 4) <= f(1, 1, 8, 8, 128, 1 << 20)
 
