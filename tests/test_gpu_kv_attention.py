@@ -450,3 +450,67 @@ def test_a_block_step():
     tol = 2 * (hq * dim + 4) * 2.0 ** -24 * size + 2 * 2.0 ** -24 * ref.abs() + 2.0 ** -8 * ref.abs()
     assert bool(((y.double() - ref).abs() <= tol).all())
     assert math.isfinite(float(y.float().sum()))
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_pages_and_rows_that_are_shared(new):
+    """Two sequences with one prefix's pages, and queries that are one row seen
+    several times (no distance between tokens)."""
+    s = Setup([(300, new), (300, new)], 2, 64, 16, BF16, E4M3, seed=25)
+    shared = (300 - new) // 16
+    s.table[1, :shared] = s.table[0, :shared]
+    for x in (s.k, s.v):
+        x[1][:shared * 16] = x[0][:shared * 16]
+    s.write()  # both write the shared pages, with the same rows
+    q = torch.randn(1, 8, 64, generator=gen(26), device=DEV).to(BF16).expand(2 * new, 8, 64)
+    y = attend(s, q)
+    torch.cuda.synchronize()
+    compare(s, q, y)
+
+
+@pytest.mark.parametrize("types", [(F16, E4M3), (F16, F16)], ids=["f16-e4m3", "f16"])
+@pytest.mark.parametrize("new", [1, 50])
+def test_rows_at_the_end_of_the_range(new, types):
+    """Keys and values up to 60000 in fp16, whose codes stand for up to 61440; and
+    rows near the least that fp16 holds."""
+    dtype, cdt = types
+    for size, qsize in ((60000.0, 3e-5), (1e-4, 60.0)):
+        s = Setup([(200, new)], 1, 64, 16, dtype, cdt, seed=27)
+        for x in (s.k, s.v):
+            x[0].copy_((torch.rand(x[0].shape, generator=gen(28), device=DEV) * 2 - 1) * size)
+            x[0][:, :, 0] = size
+        s.write()
+        q = (torch.randn(new, 4, 64, generator=gen(29), device=DEV) * qsize).to(dtype)
+        y = attend(s, q)
+        torch.cuda.synchronize()
+        if size < 1 and cdt == E4M3:
+            # Codes widen to half their value, which fp16 rounds by up to 2^-25 there: 2^-24 of
+            # a value.  A score is off by 64 / 8 max |q| of those, a weight and their sum by a
+            # factor of that each, the result by one more of V's own.
+            k, v = s.held(0)
+            ref, weight = attention64(q, k, v, seen_causal(200, new, 0, 0), 64 ** -0.5)
+            off = 2.0 ** -24 * (1 + 2 * 8 * float(q.abs().max()) * weight)
+            check_sequence(new, y.double(), ref, tolerance(ref, weight, q, k, 200, dtype, 64 ** -0.5) + off)
+        else:
+            compare(s, q, y)
+
+
+def test_many_sequences():
+    """20000 sequences, most of one token, counted through by every workgroup."""
+    n = 20000
+    lengths = [1 + (i * 7) % 5 for i in range(n)]
+    new = [1 if i % 1000 else min(3, lengths[i]) for i in range(n)]
+    k = torch.randn(n, 1, 8, 64, generator=gen(30), device=DEV).to(BF16)
+    v = torch.randn(n, 1, 8, 64, generator=gen(31), device=DEV).to(BF16)
+    cache = ct.KVCache(k, v)
+    first = [0]
+    for c in new:
+        first.append(first[-1] + c)
+    q = torch.randn(first[-1], 2, 64, generator=gen(32), device=DEV).to(BF16)
+    y = ct.kv_attention(q, cache, ints(lengths), starts=ints(first))
+    torch.cuda.synchronize()
+    for i in [0, 1, 2, 63, 64, 999, 1000, 1001, 12000, 19998, 19999]:
+        kk, vv = (t[i, :, :lengths[i]].transpose(0, 1).double() for t in (k, v))
+        qi = q[first[i]:first[i + 1]]
+        ref, size = attention64(qi, kk, vv, seen_causal(lengths[i], new[i], 0, 0), 64 ** -0.5)
+        check_sequence(i, y[first[i]:first[i + 1]].double(), ref, tolerance(ref, size, qi, kk, lengths[i], BF16, 64 ** -0.5))
