@@ -507,10 +507,11 @@ typedef struct ct_kv_batch {
  * positive, strides that are negative or let rows of the cache (or of k and v, when
  * they are written) overlap, an unknown dtype, scales missing (or given without
  * CT_E4M3), more sequences than pages without a table, tokens that the
- * sequences do not divide without starts, or one place for the cache's k and v; CT_ERR_UNSUPPORTED for a dim that is no
- * multiple of 16 or above 256, 2^26 rows (tokens x heads) or more, or more than
- * 2^30 places a sequence, 2^24 sequences (2^16 with starts) or 2^16 heads;
- * CT_ERR_HIP on a launch failure.  Asynchronous on `stream`. */
+ * sequences do not divide without starts, or one place for the cache's k and v or
+ * for their scales; CT_ERR_UNSUPPORTED for a dim that is no multiple of 16 or above
+ * 256, 2^26 rows (tokens x heads) or more, or more than 2^30 places a sequence,
+ * 2^24 sequences (2^16 with starts) or 2^16 heads; CT_ERR_HIP on a launch failure.
+ * Asynchronous on `stream`. */
 int ct_kv_write(const ct_kv_cache* cache, const ct_kv_batch* batch, const void* k,
                 long long k_token, long long k_head, const void* v, long long v_token,
                 long long v_head, int dtype, void* stream);

@@ -139,6 +139,8 @@ int rows_call(const ct_kv_cache* cache, const ct_kv_batch* batch, const void* k,
     st = check_rows("k", k, k_token, k_head, n, p.c.heads, p.c.dim, dtype, !write);
     if (st == CT_OK) st = check_rows("v", v, v_token, v_head, n, p.c.heads, p.c.dim, dtype, !write);
     if (st == CT_OK && write && cache->k == cache->v) return fail(CT_ERR_INVALID_ARG, "cache: k and v must not be the same");
+    if (st == CT_OK && write && cache->dtype == CT_E4M3 && cache->k_scale == cache->v_scale)
+        return fail(CT_ERR_INVALID_ARG, "cache: k_scale and v_scale must not be the same");
     if (st == CT_OK && !write && k == v) return fail(CT_ERR_INVALID_ARG, "k and v must not be the same");
     if (st == CT_OK && (k == cache->k || k == cache->v || v == cache->k || v == cache->v))
         return fail(CT_ERR_INVALID_ARG, "k and v must not be the cache's own");

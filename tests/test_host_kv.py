@@ -119,6 +119,10 @@ def test_one_place_for_keys_and_values_is_not_written():
     assert write(dict(CACHE, v=P)) == ct.CT_ERR_INVALID_ARG and "must not be the same" in ct.ct_last_error()
 
 
+def test_one_place_for_both_scales_is_not_written():
+    assert write(dict(Q8, v_scale=3 * P)) == ct.CT_ERR_INVALID_ARG and "k_scale and v_scale" in ct.ct_last_error()
+
+
 def test_rows_read_to_one_place_are_refused():
     assert write(read=True, v=7 * P) == ct.CT_ERR_INVALID_ARG
     assert write(read=True, k_token=64) == ct.CT_ERR_INVALID_ARG
