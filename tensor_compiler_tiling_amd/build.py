@@ -75,6 +75,8 @@ ATTENTION_CHECK = os.path.join(ASAN_DIR, "attention_check")
 HOST_CHECK_SRC = os.path.join(ROOT, "tests", "sanitize", "host_check.cpp")
 BLOCK_CHECK_SRC = os.path.join(ROOT, "tests", "sanitize", "block_check.cpp")
 ATTENTION_CHECK_SRC = os.path.join(ROOT, "tests", "sanitize", "attention_check.cpp")
+PLACEMENT_CHECK = os.path.join(ASAN_DIR, "placement_check")
+PLACEMENT_CHECK_SRC = os.path.join(ROOT, "tests", "sanitize", "placement_check.cpp")
 HOST_SRCS = sorted(glob.glob(os.path.join(CSRC, "*.cpp")))  # the library's host logic
 # sanitizers on the host side only: the device code is built as usual
 SANITIZE = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
@@ -95,7 +97,8 @@ def build_host_check() -> str:
     flags = ["-O1", "-g", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
              "-Wno-unused-command-line-argument", "-I", os.path.join(ROOT, "include"), "-I", CSRC]
-    mains = {HOST_CHECK: HOST_CHECK_SRC, BLOCK_CHECK: BLOCK_CHECK_SRC, ATTENTION_CHECK: ATTENTION_CHECK_SRC}
+    mains = {HOST_CHECK: HOST_CHECK_SRC, BLOCK_CHECK: BLOCK_CHECK_SRC, ATTENTION_CHECK: ATTENTION_CHECK_SRC,
+             PLACEMENT_CHECK: PLACEMENT_CHECK_SRC}
     rt_objs = [os.path.join(ASAN_DIR, os.path.basename(h) + ".o") for h in HOST_SRCS]
     cmds = [[HIPCC] + flags + SANITIZE + ["-x", "hip", "-c", h, "-o", o] for h, o in zip(HOST_SRCS, rt_objs)]
     cmds += [[HIPCC] + flags + SANITIZE + ["-c", src, "-o", exe + ".o"] for exe, src in mains.items()]

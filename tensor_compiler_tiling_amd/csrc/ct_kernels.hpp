@@ -79,8 +79,8 @@ struct IgemmVariant {
     // null (the legality check), then the bytes for a 16-byte aligned w
     long long (*aux_bytes)(const ConvParams& p);
     // nonzero: the variant keeps each tile's split reduction inside one XCD,
-    // relying on workgroup b running on XCD b % 8; legal only where the
-    // runtime has observed that placement
+    // relying on workgroups of one number mod 8 running on one XCD; legal only
+    // where the runtime has observed that placement
     int xcd_local;
     // nonzero: the width (output pixels) of the variant's column tiles, when
     // it is not waves_n * reps_n * mfma_n
@@ -119,6 +119,19 @@ hipError_t launch_bcast_flat(const float* var, void* out, int N, int C, int HW,
 
 // out[b] = the XCD that workgroup b of a `blocks`-workgroup launch ran on.
 hipError_t launch_xcc_probe(int* out, int blocks, hipStream_t stream);
+
+// Whether such a launch was dealt out in turn: eight XCDs, and workgroups of
+// one number mod 8 on one of them.  Which XCD is first does not matter: a queue
+// whose earlier launches were no whole multiples of 8 workgroups goes on where
+// it stopped (b + 7 mod 8, say), and no kernel asks for an XCD by number.
+inline bool placed_round_robin(const int* xcd, int blocks) {
+    unsigned seen = 0;
+    for (int b = 0; b < blocks; ++b) {
+        if (xcd[b] < 0 || xcd[b] > 7 || xcd[b] != xcd[b % 8]) return false;
+        seen |= 1u << xcd[b];
+    }
+    return seen == 0xff;
+}
 
 // Deterministic device fill used by the tuner's scratch inputs:
 // v[i] = lo + (hi - lo) * u(i, seed), u a counter-based hash in [0, 1).

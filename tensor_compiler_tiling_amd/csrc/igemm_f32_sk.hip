@@ -84,7 +84,7 @@ constexpr int kSkipL1 = 1;             // cache policy: sc0, the load misses the
 //   fd_wstr = OH*OW, fd_wp = Wp, fd_rwp = XCS, fd_hp = Hp, fd_ow = OW,
 //   fd_t = KH*KW, fd_kw = KW.
 // XL: XCD-local split reduction -- every split of a tile has the same
-// workgroup index mod 8, so on an MI355X (workgroup b on XCD b % 8) the
+// workgroup index mod 8, so on an MI355X (equal numbers mod 8 share an XCD) the
 // partial stores, the ticket and the partial loads complete in that XCD's
 // L2 rather than at device scope; legal only where the runtime has observed
 // that placement.

@@ -40,13 +40,13 @@
 // XCD-local form (XL).  Each round trip of that protocol at device scope --
 // the coherent partial store, the ticket, the reducer's loads -- goes past
 // the L2 of the workgroup's XCD and costs about half a microsecond.  On an
-// MI355X workgroup b runs on XCD b % 8, and each XCD's L2 is the coherence
+// MI355X workgroups of one number mod 8 run on one XCD, and each XCD's L2 is the coherence
 // point of its CUs.  The XL form gives all S workgroups of a tile the same
 // b % 8 (tile = b%8 + 8*((b/8)/S), split = (b/8) % S), so the protocol runs
 // through that one L2: plain stores, a workgroup-scope atomic (executed in
 // L2), loads that skip the CU's L1.  Kernel boundaries write the L2 back.
 // The runtime enables XL variants only on a device where a probe launch
-// has observed the b % 8 placement.
+// has observed that placement.
 #include "ct_device.hpp"
 #include "igemm_common.hpp"
 

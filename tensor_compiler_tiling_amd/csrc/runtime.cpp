@@ -359,7 +359,7 @@ static __device__ int g_probe_out[kProbeBlocks];
 
 struct DeviceState {
     bool ready = false;
-    bool xcd_rr = false;          // workgroup b runs on XCD b % 8
+    bool xcd_rr = false;          // workgroups of one number mod 8 run on one XCD
     const void* zero = nullptr;   // device address of g_zero_page
 };
 
@@ -392,10 +392,8 @@ int device_setup_locked(int dev) {
     bool rr = false;
     if (launch_xcc_probe(probe, kProbeBlocks, ps) == hipSuccess &&
         hipMemcpyAsync(h.data(), probe, kProbeBlocks * sizeof(int), hipMemcpyDeviceToHost, ps) == hipSuccess &&
-        hipStreamSynchronize(ps) == hipSuccess) {
-        rr = true;
-        for (int b = 0; b < kProbeBlocks; ++b) rr = rr && h[b] == b % 8;
-    }
+        hipStreamSynchronize(ps) == hipSuccess)
+        rr = placed_round_robin(h.data(), kProbeBlocks);
     (void)hipStreamDestroy(ps);
     (void)hipGetLastError();
     d.zero = z;
@@ -427,7 +425,7 @@ int ensure_device(hipStream_t stream, int* dev_out) {
     return device_setup_locked(dev);
 }
 
-// Whether workgroup b of a launch runs on XCD b % 8 on the current device
+// Whether workgroups of one number mod 8 run on one XCD on the current device
 // (false if the probe failed).  On a host with no device nothing can launch,
 // and the tuning log's XCD-local records are taken as they were measured;
 // any launch happens on a device, where the probe decides.
