@@ -150,15 +150,27 @@ __device__ __forceinline__ uint4v load16(const char* p) {
     return v;
 }
 
-// Values that are not finite become 0: was there any?
-template <int DT>
-__device__ __forceinline__ bool clear_not_finite(uint4v& v) {
-    constexpr unsigned E = DT == DT_F16 ? 0x7c00u : 0x7f80u;
-    bool bad = false;
+// Values that are not finite become 0; what is returned is not 0 if there was any.
+// 16-bit caches by arithmetic on both halves of a dword: adding one in the exponent's
+// last place carries into the sign's exactly where all of the exponent is ones.
+// Compares have a lane mask a value alive, for which the row forms' scalars did not
+// suffice (128 wide 140 spilled, 4 so; one token of 1200 12.3 -> 11.1 us, windows 28.4 ->
+// 24.5).  Between the widening of 8-bit rows compares are the faster (trees 32 x 64
+// 155 us and 163, 16 x 8 tokens over 4096 58.3 and 59.7) and spill nothing in the loop.
+template <int DT, bool Q8>
+__device__ __forceinline__ unsigned clear_not_finite(uint4v& v) {
+    constexpr unsigned E = DT == DT_F16 ? 0x7c00u : 0x7f80u, ONE = DT == DT_F16 ? 0x04000400u : 0x00800080u;
+    unsigned bad = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if ((v[i] & E) == E) v[i] &= 0xffff0000u, bad = true;
-        if (((v[i] >> 16) & E) == E) v[i] &= 0xffffu, bad = true;
+        if constexpr (Q8) {
+            if ((v[i] & E) == E) v[i] &= 0xffff0000u, bad = 1;
+            if (((v[i] >> 16) & E) == E) v[i] &= 0xffffu, bad = 1;
+        } else {
+            const unsigned hit = ((v[i] & (E << 16 | E)) + ONE) & 0x80008000u;
+            v[i] &= ~((hit - (hit >> 15)) | hit);
+            bad |= hit;
+        }
     }
     return bad;
 }
@@ -504,13 +516,13 @@ __global__ __launch_bounds__(WAVES * 64, (DP > 128 ? 1 : 2)) void attend_tile_ke
         for (int j = 0; j < NP; ++j) {
             if (ALL % NT && key_of(j) >= KT) continue;
             const float f = Q8 ? s_scale[(i - from) % (2 * WAVES)][key_of(j)][1] : 1.0f;
-            bool bad = false;
+            unsigned bad = 0;
 #pragma unroll
             for (int e = 0; e < (Q8 ? 2 : 1); ++e) {
                 uint4v v = Q8 ? widen8<DT>(rv[j], e, f) : rv[j];
                 if (!whole) {
                     if (k0 + key_of(j) >= t.len) v = uint4v{0, 0, 0, 0};
-                    bad |= clear_not_finite<DT>(v);
+                    bad |= clear_not_finite<DT, Q8>(v);
                 }
                 *reinterpret_cast<uint4v*>(s_v[buf] + key_of(j) * VP + piece_of(j) * PIECE + 8 * e) = v;
             }
@@ -765,7 +777,7 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendParams p) {
     for (int i = from + wave; i < to; i += WAVES) {
         const int k0 = keys.at(i) * KT;
         const bool whole = all_seen<KT>(p, t, i0, i1, k0);
-        unsigned bad = 0;  // keys whose V is not finite
+        unsigned hit[2] = {0, 0};  // whether V of the lane's keys is not finite
         // V to LDS, and the first product: both free their registers
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -778,19 +790,19 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendParams p) {
                     uint4v v = Q8 ? widen8<DT>(rv[h][j], e, sv[h]) : rv[h][j];
                     if (!whole) {
                         if (k0 + k >= t.len) v = uint4v{0, 0, 0, 0};
-                        if (clear_not_finite<DT>(v)) bad |= 1u << k;
+                        hit[h] |= clear_not_finite<DT, Q8>(v);
                     }
                     *reinterpret_cast<uint4v*>(s_v + k * PITCH + (4 * j + quad) * PIECE + 8 * e) = v;
                 }
             }
         floatx4 z[2];
-z[0] = z[1] = floatx4{};
+        z[0] = z[1] = floatx4{};
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int s = 0; s < DS; ++s) {
                 const uint4v a = Q8 ? widen8<DT>(rk[h][s / 2], s % 2, sk[h]) : rk[h][s];
-z[h] = mma16<DT>(a, q[s], z[h]);
+                z[h] = mma16<DT>(a, q[s], z[h]);
             }
         if (i + WAVES < to) {
             load_rows(i + WAVES);
@@ -840,6 +852,7 @@ z[h] = mma16<DT>(a, q[s], z[h]);
             o[d] = mma16<DT>(v, w, o[d]);
         }
         wave_fence();  // and written anew once they have
+        const unsigned bad = (hit[0] ? 1u << col : 0) | (hit[1] ? 0x10000u << col : 0);
         if (__any(bad)) {
 #pragma unroll 1
             for (int k = 0; k < KT; ++k) {
