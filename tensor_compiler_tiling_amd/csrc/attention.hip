@@ -702,8 +702,8 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendParams p) {
     constexpr int DS = NK * (Q8 ? 2 : 1);  // instructions of the first product
     constexpr int DO = DP / 16;
     constexpr int VLDS = KT * PITCH * 2, OLDS = ROWS * (DP + 4) * 4;
-    constexpr int SETS = OLDS * WAVES <= VLDS * WAVES + 4096 ? WAVES : 1;  // of the waves' sums at the end
-    __shared__ __attribute__((aligned(16))) char s_mem[VLDS * WAVES > OLDS * SETS ? VLDS * WAVES : OLDS * SETS];
+    static_assert(OLDS <= VLDS, "all waves' sums have room side by side at the end");
+    __shared__ __attribute__((aligned(16))) char s_mem[VLDS * WAVES];
     __shared__ float s_ml[WAVES][ROWS][2];
 
     const int head = blockIdx.x % p.c.heads;
@@ -887,26 +887,17 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendParams p) {
     const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - mx);
 #pragma unroll
     for (int d = 0; d < DO; ++d) o[d] *= f;
-    // SETS of the waves' sums have room side by side; the waves beyond add to those
 #pragma unroll
-    for (int w0 = 0; w0 < WAVES; w0 += SETS) {
-        if (wave >= w0 && wave < w0 + SETS) {
-#pragma unroll
-            for (int d = 0; d < DO; ++d) {
-                floatx4* at = reinterpret_cast<floatx4*>(s_o + (wave - w0) * OLDS / 4 + col * (DP + 4) + d * 16 + quad * 4);
-                if (w0 == 0) *at = o[d];
-                else *at += o[d];
-            }
-        }
-        __syncthreads();
-    }
+    for (int d = 0; d < DO; ++d)
+        *reinterpret_cast<floatx4*>(s_o + wave * OLDS / 4 + col * (DP + 4) + d * 16 + quad * 4) = o[d];
+    __syncthreads();
     const float inv = inverse<DT, Q8>(total);
 #pragma unroll
     for (int d = 0; d < DO; ++d) {
         if (d % WAVES != wave) continue;
         floatx4 v = {};
 #pragma unroll
-        for (int w = 0; w < SETS; ++w)
+        for (int w = 0; w < WAVES; ++w)
             v += *reinterpret_cast<const floatx4*>(s_o + w * OLDS / 4 + col * (DP + 4) + d * 16 + quad * 4);
         put4<DT>(p, row, part, d * 16 + quad * 4, v[0], v[1], v[2], v[3], inv);
     }
