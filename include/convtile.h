@@ -540,7 +540,8 @@ typedef struct ct_kv_mask {
 
 /* Attention of the new tokens over the cache, which holds them already:
  *   y = sum_j exp(scale q . k_j) v_j / sum_j exp(scale q . k_j)
- * over the places j that a token sees; zeros where it sees none.  q and y are
+ * over the places j that a token sees; zeros where it sees none, NaN where all that
+ * it sees have a score of -infinity (0 / 0).  q and y are
  * [tokens][heads][dim] of `dtype` (CT_F16 or CT_BF16, that of a 16-bit cache);
  * `heads` is a multiple of the cache's, whose head h the heads h * heads / cache
  * heads and following share.  mask may be NULL (causal).  max_len: the longest

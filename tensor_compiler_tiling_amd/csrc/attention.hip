@@ -312,6 +312,29 @@ __device__ __forceinline__ unsigned long long seen(const AttendParams& p, const 
     return m & bits_between(0, all);
 }
 
+// Does a row see any of keys [a, b)?
+__device__ __forceinline__ bool sees_any(const AttendParams& p, const Tile& t, const Row& row, int a, int b) {
+    if (a < 0) a = 0;
+    if (b > t.len) b = t.len;
+    const int end = (p.tree ? t.ctx - 1 : row.pos) + 1, low = row.pos - p.window + 1, last = b < end ? b : end;
+    bool any = (a > low ? a : low) < last || a < (last < p.sinks ? last : p.sinks);
+    if (p.tree)
+        for (int k = a > t.ctx ? a : t.ctx; k < b; k += 64) any |= (seen(p, t, row, k) & bits_between(0, b - k)) != 0;
+    return row.token >= 0 && any;
+}
+
+// The maximum of a row in stages [from, to) that has found none: -infinity where it
+// sees nothing there, else the least number.  All its scores are then -infinity (or
+// NaN, as its sums are), and unless others have a greater maximum, its result is
+// 0 / 0 and not that of a row that sees nothing.
+template <int KT>
+__device__ __forceinline__ float least_maximum(const AttendParams& p, const Tile& t, const Row& row, const Keys& keys, int from, int to) {
+    bool any = false;
+    if (from < keys.sinks) any |= sees_any(p, t, row, from * KT, (to < keys.sinks ? to : keys.sinks) * KT);
+    if (to > keys.sinks) any |= sees_any(p, t, row, keys.at(from > keys.sinks ? from : keys.sinks) * KT, (keys.at(to - 1) + 1) * KT);
+    return any ? -0x1.fffffep127f : -INFINITY;
+}
+
 // Does every row among tokens [i0, i1] see all of keys [k0, k0 + KT)?
 template <int KT>
 __device__ __forceinline__ bool all_seen(const AttendParams& p, const Tile& t, int i0, int i1, int k0) {
@@ -367,10 +390,11 @@ __device__ __forceinline__ void put_weight(const AttendParams& p, const Row& row
     p.part_ml[2 * at + 1] = l;
 }
 
-// 1 / l, 0 for a row that sees nothing.  With fp16 and 8 bits V is half (above).
+// 1 / l, 0 for a row that sees nothing (whose maximum is none).  With fp16 and 8 bits
+// V is half (above).
 template <int DT, bool Q8>
-__device__ __forceinline__ float inverse(float l) {
-    return l == 0.0f ? 0.0f : (DT == DT_F16 && Q8 ? 2.0f : 1.0f) / l;
+__device__ __forceinline__ float inverse(float l, float m) {
+    return m == -INFINITY ? 0.0f : (DT == DT_F16 && Q8 ? 2.0f : 1.0f) / l;
 }
 
 // Key tiles of a part: none for the last parts where there are few.
@@ -675,7 +699,8 @@ __global__ __launch_bounds__(WAVES * 64, (DP > 128 ? 1 : 2)) void attend_tile_ke
         add_not_finite(to - 1);
     }
     l += __shfl_xor(l, 32);
-    const float inv = inverse<DT, Q8>(l);
+    if (__any(m == -INFINITY)) m = m == -INFINITY ? least_maximum<KT>(p, t, row, keys, from, to) : m;
+    const float inv = inverse<DT, Q8>(l, m);
 #pragma unroll
     for (int d = 0; d < DO; ++d)
 #pragma unroll
@@ -885,13 +910,14 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendParams p) {
         total += mw == -INFINITY ? 0.0f : s_ml[w][col][1] * __builtin_amdgcn_exp2f(mw - mx);
     }
     const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - mx);
+    if (__any(mx == -INFINITY)) mx = mx == -INFINITY ? least_maximum<KT>(p, t, row, keys, from, to) : mx;
 #pragma unroll
     for (int d = 0; d < DO; ++d) o[d] *= f;
 #pragma unroll
     for (int d = 0; d < DO; ++d)
         *reinterpret_cast<floatx4*>(s_o + wave * OLDS / 4 + col * (DP + 4) + d * 16 + quad * 4) = o[d];
     __syncthreads();
-    const float inv = inverse<DT, Q8>(total);
+    const float inv = inverse<DT, Q8>(total, mx);
 #pragma unroll
     for (int d = 0; d < DO; ++d) {
         if (d % WAVES != wave) continue;
@@ -961,7 +987,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p) {
 #pragma unroll
         for (int w = 1; w < W; ++w) sum += s_o[w][lane];
     }
-    const float inv = inverse<DT, Q8>(total);
+    const float inv = inverse<DT, Q8>(total, mx);
     if (!on) return;
     const uint2v w = {pack2<DT>(sum[0] * inv, sum[1] * inv), pack2<DT>(sum[2] * inv, sum[3] * inv)};
     __builtin_memcpy(p.y + token * p.y_token + head * p.y_head + lane * 8, &w, 8);

@@ -1,0 +1,84 @@
+"""GPU tests of attention over rows that are not finite, at the ends of the
+definition y = sum exp(z) v / sum exp(z): what a token sees counts, however the
+call's keys are divided, and what it does not see has no part in its result."""
+import pytest
+import torch
+
+from tensor_compiler_tiling_amd import convtile as ct
+
+from _gpu_helpers import DEV
+from _kv_helpers import BF16, E4M3, F16, F32, Setup, attention64, check_sequence, gen, ints, seen_causal, seen_tree, tolerance, tree_bits
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    assert torch.cuda.is_available(), "GPU test run without a GPU"
+    torch.cuda.init()
+    yield
+    torch.cuda.synchronize()
+
+
+def check(name, s, q, y, see, k=None, v=None):
+    """One sequence against 64 bits.  Rows whose seen scores are all -inf are NaN,
+    0 / 0; scores of -inf beside others have no weight."""
+    hk, hv = s.held(0)
+    k, v = hk if k is None else k, hv if v is None else v
+    dark = (k == -INF).any(dim=2)  # [length, heads]: q is positive there
+    n, hq, d = q.shape
+    g = hq // s.heads
+    for j in range(s.heads):
+        lit = see & ~dark[:, j][None]
+        kj = torch.where(k[:, j:j + 1].isfinite(), k[:, j:j + 1], torch.zeros_like(k[:, j:j + 1]))
+        vj = v[:, j:j + 1]
+        qj, yj = q[:, j * g:(j + 1) * g], y[:, j * g:(j + 1) * g].double()
+        nan = see.any(dim=1) & ~lit.any(dim=1)
+        assert bool(yj[nan].isnan().all()), (name, "all scores -inf")
+        assert bool((yj[~see.any(dim=1)] == 0).all()), (name, "nothing seen")
+        ref, size = attention64(qj, kj, vj, lit, d ** -0.5)
+        fin = torch.where(ref.isfinite(), ref, torch.zeros_like(ref))
+        tol = tolerance(fin, size, qj, kj, k.shape[0], q.dtype, d ** -0.5)
+        check_sequence(name, yj[~nan], ref[~nan], tol[~nan])
+
+
+# new tokens and heads of a group: one row, 16 rows, several tiles of rows
+ROWS = [(1, 1), (4, 4), (40, 4), (300, 2)]
+
+
+@pytest.mark.parametrize("tree", [False, True], ids=["causal", "tree"])
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=str)
+@pytest.mark.parametrize("new,group", ROWS)
+@pytest.mark.parametrize("length,window,sinks", [(300, 0, 0), (300, 70, 3), (3000, 0, 0), (3000, 400, 2)])
+def test_scores_of_minus_infinity(length, window, sinks, new, group, dtype, tree):
+    s = Setup([(length, new)], 2, 64, 64, dtype, dtype, seed=new)
+    # head 0: every key; head 1: all but the last `new` keys, so that rows differ by what they see behind
+    s.k[0][:, 0, 5] = -INF
+    s.k[0][:length - new + new // 3 + 1, 1, 5] = -INF
+    s.write()
+    q = torch.randn(new, 2 * group, 64, generator=gen(1), device=DEV).to(dtype)
+    q[:, :, 5] = 1.0
+    see, bits = seen_causal(length, new, window, sinks), None
+    if tree:
+        sees = torch.rand(new, new, generator=torch.Generator().manual_seed(2)) < 0.3
+        sees[new // 2] = False
+        see, bits = seen_tree(length, new, window, sinks, sees), tree_bits(sees, (new + 63) // 64)
+    for longest in (None, 1, length, 64 * length):
+        y = ct.kv_attention(q, s.cache, s.lens, s.table, max_len=longest, window=window, sinks=sinks, tree=bits)
+        torch.cuda.synchronize()
+        check(longest, s, q, y, see)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=str)
+def test_scores_of_minus_infinity_beside_rows_that_see_nothing(dtype):
+    """More new tokens than places: the first see nothing and give zeros."""
+    for new, group in ROWS[1:]:
+        s = Setup([(new, new)], 2, 64, 16, dtype, dtype, seed=3)
+        s.k[0][:, :, 5] = -INF
+        s.write()
+        q = torch.ones(new, 2 * group, 64, dtype=dtype, device=DEV)
+        y = ct.kv_attention(q, s.cache, ints([new - 2]), s.table)
+        torch.cuda.synchronize()
+        assert bool((y[:2] == 0).all()) and bool(y[2:].isnan().all()), new

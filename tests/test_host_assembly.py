@@ -93,7 +93,7 @@ def test_attention_has_its_registers(tmp_path):
     for name, scratch, scalars, vectors in kernels:
         assert (int(scratch), int(vectors)) == (0, 0), name
         # strides and pointers that live through the whole kernel
-        assert int(scalars) <= 48, (name, scalars)
+        assert int(scalars) <= 64, (name, scalars)
 
 
 SKIPPED = """
