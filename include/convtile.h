@@ -549,8 +549,8 @@ typedef struct ct_kv_mask {
  * Sums, maximum and weights are fp32; the weights are rounded to `dtype` for the
  * product with v.  With CT_F16 and 8-bit rows, these must stay within the
  * range of fp16.  What lies in places that a token does not see has no part in its
- * result, whatever it is; NaN and infinities that it sees do.  A page number
- * outside of the pool is read as page 0.
+ * result, whatever it is; NaN and infinities that it sees do, those of v (in 16 bits)
+ * whatever their weight.  A page number outside of the pool is read as page 0.
  * Few tokens have their keys split over workgroups, whose sums are joined in
  * order: a result depends on the sizes and the batch's contents and repeats
  * bit for bit.  That needs `workspace`, of at least

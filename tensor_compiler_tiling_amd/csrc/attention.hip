@@ -115,10 +115,13 @@ __device__ __forceinline__ T in_place(T v) {
     return v;
 }
 
-// What sums at maximum m are scaled by for a greater one: at least the least
-// normal number, so that what is infinite stays so.
-__device__ __forceinline__ float fall_to(float m, float next) {
-    return m == -INFINITY ? 1.0f : fmaxf(__builtin_amdgcn_exp2f(m - next), 0x1p-126f);
+// What sums at maximum m are scaled by for a greater one; 0 past 2^-126.
+__device__ __forceinline__ float fall_to(float m, float next) { return m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - next); }
+
+// A sum of a wave or part at the common maximum: what is infinite stays so (in 8 bits
+// nothing is).
+__device__ __forceinline__ float fallen(float o, float fall) {
+    return fall == 0.0f && !__builtin_isfinite(o) ? o : o * fall;
 }
 
 // The greater of a lane's value and that of the lane 32 away.
@@ -367,6 +370,96 @@ struct CacheRow {
         return __builtin_isfinite(f) ? 0.0f : f;
     }
 };
+
+// Which of keys k0 to k0 + KT - 1 have values that are infinite (or not finite), as
+// bits: a key a lane, 16-bit caches only.
+template <int DT, int KT>
+__device__ __forceinline__ unsigned long long keys_with(const AttendParams& p, const Tile& t, int head, int k0, bool nan_too) {
+    constexpr unsigned E = DT == DT_F16 ? 0x7c007c00u : 0x7f807f80u, ONE = DT == DT_F16 ? 0x04000400u : 0x00800080u;
+    const int key = k0 + (int)(threadIdx.x & 63) % KT;
+    const CacheRow<DT, false> row(p, t, head, key < t.len ? key : t.len - 1);
+    unsigned hit = 0;
+#pragma unroll 1
+    for (int d = 0; d < p.c.dim; d += 16) {
+        const uint4v v[2] = {load16(row.v + 2 * d), load16(row.v + 2 * d + 16)};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const unsigned u = v[i / 4][i % 4];
+            // both halves: all ones in the exponent carry, and so does what is not E's pattern
+            hit |= nan_too ? (u & E) + ONE : ~(((u & 0x7fff7fffu) ^ E) + 0x7fff7fffu);
+        }
+    }
+    const unsigned long long all = __ballot((hit & 0x80008000u) && key < t.len);
+    return KT == 64 ? all : all & ((1ull << KT) - 1);
+}
+
+// An infinity of V that a row sees makes its sum infinite, however small its weight.
+// But a weight that rounds to 0 (below 2^-31 of the largest in fp16) gives NaN in the
+// product, as does an infinite sum whose scale falls to 0; and which keys share a
+// maximum depends on how they are divided.  So if there are infinities in the wave's
+// stages from, from + step, ... below to, sums (column + off(d, e) in o[d][e]) that have
+// become NaN are made anew from what is not finite in the cache; those in which
+// nothing is stay NaN.  (To look for infinities in every stage as V is brought to LDS
+// cost 5 to 12%.)
+template <int DT, int KT, typename V, int N, typename F>
+__device__ __forceinline__ void mend_nan(const AttendParams& p, const Tile& t, const Row& row, const Keys& keys, int head, int from,
+                                         int to, int step, V (&o)[N], float l, int column, F off) {
+    constexpr int E = sizeof(V) / 4;
+    float sum = 0.0f;  // NaN if any of them is, or is infinite
+#pragma unroll
+    for (int d = 0; d < N; ++d)
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum = fmaf(o[d][e], 0.0f, sum);
+    // where the weights are NaN, all is
+    if (__builtin_expect(!__any(sum != sum && l == l && row.token >= 0), 1)) return;
+    unsigned made[(N * E + 31) / 32] = {}, any = 0;
+#pragma unroll
+    for (int d = 0; d < N; ++d)
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int n = d * E + e;
+            made[n / 32] |= (o[d][e] != o[d][e] ? 1u : 0u) << n % 32;
+        }
+#pragma unroll
+    for (unsigned m : made) any |= m;
+    if (!__any(any && row.token >= 0)) return;
+    bool infinite = false;
+#pragma unroll 1
+    for (int i = from; i < to && !infinite; i += step) infinite = keys_with<DT, KT>(p, t, head, keys.at(i) * KT, false) != 0;
+    if (!infinite) return;
+#pragma unroll
+    for (int d = 0; d < N; ++d)
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[d][e] = o[d][e] != o[d][e] ? 0.0f : o[d][e];
+#pragma unroll 1
+    for (int i = from; i < to; i += step) {
+        const int k0 = keys.at(i) * KT;
+        const unsigned long long bits = seen(p, t, row, k0);
+#pragma unroll 1
+        for (unsigned long long bad = keys_with<DT, KT>(p, t, head, k0, true); bad; bad &= bad - 1) {
+            const int k = __builtin_ctzll(bad);
+            const CacheRow<DT, false> v(p, t, head, k0 + k);
+            const unsigned on = 0u - (unsigned)(bits >> k & 1);
+            const int d0 = in_place(column);
+#pragma unroll
+            for (int d = 0; d < N; ++d) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const int n = d * E + e;
+                    const unsigned mask = on & (0u - (made[n / 32] >> n % 32 & 1));
+                    o[d][e] = in_place(o[d][e] + __uint_as_float(__float_as_uint(v.not_finite(d0 + off(d, e))) & mask));
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int d = 0; d < N; ++d)
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int n = d * E + e;
+            o[d][e] = (made[n / 32] >> n % 32 & 1) && o[d][e] == 0.0f ? __builtin_nanf("") : o[d][e];
+        }
+}
 
 // ------------------------------------------------------------- the results --
 // Four neighbouring elements of a row's sums from d.
@@ -699,7 +792,9 @@ __global__ __launch_bounds__(WAVES * 64, (DP > 128 ? 1 : 2)) void attend_tile_ke
         add_not_finite(to - 1);
     }
     l += __shfl_xor(l, 32);
-    if (__any(m == -INFINITY)) m = m == -INFINITY ? least_maximum<KT>(p, t, row, keys, from, to) : m;
+    if constexpr (!Q8)  // NaN is all that is not finite in 8 bits
+        mend_nan<DT, KT>(p, t, row, keys, head, from, to, 1, o, l, 4 * half, [](int d, int e) { return d * 32 + 8 * (e / 4) + e % 4; });
+    if (__builtin_expect(__any(m == -INFINITY), 0)) m = m == -INFINITY ? least_maximum<KT>(p, t, row, keys, from, to) : m;
     const float inv = inverse<DT, Q8>(l, m);
 #pragma unroll
     for (int d = 0; d < DO; ++d)
@@ -895,6 +990,8 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendParams p) {
     // the waves' sums, brought to their common maximum and added in order
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
+    if constexpr (!Q8)  // as above
+        mend_nan<DT, KT>(p, t, row, keys, head, from + wave, to, WAVES, o, l, 4 * quad, [](int d, int e) { return d * 16 + e; });
     if (quad == 0) {
         s_ml[wave][col][0] = m;
         s_ml[wave][col][1] = l;
@@ -909,10 +1006,17 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendParams p) {
         const float mw = s_ml[w][col][0];
         total += mw == -INFINITY ? 0.0f : s_ml[w][col][1] * __builtin_amdgcn_exp2f(mw - mx);
     }
-    const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - mx);
-    if (__any(mx == -INFINITY)) mx = mx == -INFINITY ? least_maximum<KT>(p, t, row, keys, from, to) : mx;
+    const float fall = fall_to(m, mx);
+    if (__builtin_expect(__any(mx == -INFINITY), 0)) mx = mx == -INFINITY ? least_maximum<KT>(p, t, row, keys, from, to) : mx;
+    if (!Q8 && __builtin_expect(__any(fall == 0.0f), 0)) {
 #pragma unroll
-    for (int d = 0; d < DO; ++d) o[d] *= f;
+        for (int d = 0; d < DO; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[d][e] = fallen(o[d][e], fall);
+    } else {
+#pragma unroll
+        for (int d = 0; d < DO; ++d) o[d] *= fall;
+    }
 #pragma unroll
     for (int d = 0; d < DO; ++d)
         *reinterpret_cast<floatx4*>(s_o + wave * OLDS / 4 + col * (DP + 4) + d * 16 + quad * 4) = o[d];
@@ -957,7 +1061,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p) {
     float total = 0.0f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        m[i] = m[i] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[i] - mx);  // sums of no key are zeros
+        m[i] = fall_to(m[i], mx);  // sums of no key are zeros
         total += l[i] * m[i];
     }
 #pragma unroll
@@ -966,20 +1070,29 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p) {
     const bool on = lane * 4 < p.c.dim;
     const float* const at = p.part_o + (long long)r * p.c.dim + lane * 4;
     constexpr int U = 8;  // parts whose rows are on their way together
-    for (int s0 = W > 1 ? wave : 0; s0 < p.parts; s0 += U * W) {
-        floatx4 v[U];
+    auto add = [&](auto far) {
+        for (int s0 = W > 1 ? wave : 0; s0 < p.parts; s0 += U * W) {
+            floatx4 v[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int s = s0 + u * W;
-            v[u] = floatx4{};
-            if (on && s < p.parts) v[u] = *reinterpret_cast<const floatx4*>(at + s * rows * p.c.dim);
-        }
+            for (int u = 0; u < U; ++u) {
+                const int s = s0 + u * W;
+                v[u] = floatx4{};
+                if (on && s < p.parts) v[u] = *reinterpret_cast<const floatx4*>(at + s * rows * p.c.dim);
+            }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int s = s0 + u * W;
-            sum += v[u] * __shfl(s < 64 ? m[0] : m[1], s & 63);
+            for (int u = 0; u < U; ++u) {
+                const int s = s0 + u * W;
+                const float fall = __shfl(s < 64 ? m[0] : m[1], s & 63);
+                if constexpr (!decltype(far)::value) sum += v[u] * fall;
+                else
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sum[e] += fallen(v[u][e], fall);
+            }
         }
-    }
+    };
+    // maxima so far apart that a part's scale is 0 are rare (1 us a call if all went that way)
+    if (!Q8 && __builtin_expect(__any(m[0] == 0.0f || m[1] == 0.0f), 0)) add(std::true_type{});
+    else add(std::false_type{});
     if constexpr (W > 1) {
         s_o[wave][lane] = sum;
         __syncthreads();

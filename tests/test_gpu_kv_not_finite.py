@@ -82,3 +82,49 @@ def test_scores_of_minus_infinity_beside_rows_that_see_nothing(dtype):
         y = ct.kv_attention(q, s.cache, ints([new - 2]), s.table)
         torch.cuda.synchronize()
         assert bool((y[:2] == 0).all()) and bool(y[2:].isnan().all()), new
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=str)
+@pytest.mark.parametrize("new,group", ROWS)
+@pytest.mark.parametrize("length,at,dim", [(3000, 5, 64), (128, 31, 64), (700, 3, 64), (700, 3, 96), (128, 31, 128), (3000, 5, 160),
+                                           (128, 31, 256)])
+def test_infinities_that_weights_fall_far_behind(length, at, dim, new, group, dtype):
+    """Scores that grow by 200 powers of two and more along the keys, with infinite
+    values among the first: however the keys are divided, those stay infinite, as
+    their weights are above 0."""
+    if new >= length:
+        length = 3000
+    s = Setup([(length, new)], 2, dim, 64, dtype, dtype, seed=7)
+    ramp = torch.linspace(0.01, 8, length, device=DEV)[:, None, None]
+    s.k[0] = (ramp * torch.ones(length, 2, dim, device=DEV)).to(dtype)
+    s.v[0][at, 1, 3], s.v[0][at, 1, dim - 1] = INF, -INF
+    s.v[0][at, 1, 50], s.v[0][at + 1 if at == 3 else at - 1, 1, 50] = INF, -INF
+    s.v[0][at, 1, 49], s.v[0][at - 1, 1, 49] = INF, float("nan")
+    s.write()
+    q = torch.full((new, 2 * group, dim), 24 / dim ** 0.5, dtype=dtype, device=DEV)
+    see = seen_causal(length, new, 0, 0)
+    for longest in (None, 1, length):
+        y = ct.kv_attention(q, s.cache, s.lens, s.table, max_len=longest)
+        torch.cuda.synchronize()
+        z = y[:, group:]
+        assert bool((z[..., 3] == INF).all()) and bool((z[..., dim - 1] == -INF).all()), longest
+        assert bool(z[..., 49:51].isnan().all()), longest
+        check(longest, s, q, y, see)
+
+
+@pytest.mark.parametrize("new,group", ROWS)
+def test_great_values_that_weights_fall_far_behind(new, group):
+    """200 values near the end of bf16's range (whose sum fp32 still holds), then keys
+    whose scores are 2^200 times and more: the first leave the others' sums alone."""
+    length = 300
+    s = Setup([(length, new)], 1, 64, 64, BF16, BF16, seed=8)
+    s.k[0].fill_(0.0)
+    s.k[0][200:] = 8.0
+    s.v[0][:200] = 1.5e36
+    s.write()
+    q = torch.full((new, group, 64), 3.0, dtype=BF16, device=DEV)
+    see = seen_causal(length, new, 0, 0)
+    for longest in (None, 1, length):
+        y = ct.kv_attention(q, s.cache, s.lens, s.table, max_len=longest)
+        torch.cuda.synchronize()
+        check(longest, s, q, y, see)
