@@ -547,8 +547,8 @@ typedef struct ct_kv_mask {
  * heads and following share.  mask may be NULL (causal).  max_len: the longest
  * of lens if the caller knows (0 otherwise); it only guides how the work is divided.
  * Sums, maximum and weights are fp32; the weights are rounded to `dtype` for the
- * product with v.  With CT_F16 and 8-bit rows, these must stay within the
- * range of fp16.  What lies in places that a token does not see has no part in its
+ * product with v.  With CT_F16, 8-bit rows must stay within the range of fp16;
+ * what passes it counts as infinite.  What lies in places that a token does not see has no part in its
  * result, whatever it is; NaN and infinities that it sees do, those of v (in 16 bits)
  * whatever their weight.  A page number outside of the pool is read as page 0.
  * Few tokens have their keys split over workgroups, whose sums are joined in

@@ -349,24 +349,30 @@ __device__ __forceinline__ bool all_seen(const AttendParams& p, const Tile& t, i
 // A weight of 0 does not clear what is not finite.  Where some row of a stage does
 // not see all of its keys, V therefore goes into the product without such values,
 // and the rows that see one get it by this: a key's value in the cache, and of
-// it what is not finite (0 for the others).
+// it what is not finite (0 for the others).  In 8 bits that is NaN, and what its scale
+// takes past the range of the type.
 template <int DT, bool Q8>
 struct CacheRow {
     const char* v;
+    float scale;
     int dim;
     __device__ __forceinline__ CacheRow(const AttendParams& p, const Tile& t, int head, int key) : dim(p.c.dim) {
         const Place at = place_of(p.c, key);
         int page = page_of(p.b, t.seq, at.index);
         if ((unsigned)page >= (unsigned)p.c.pages) page = 0;
         v = p.c.v + page * p.c.ld_page + at.in * p.c.ld_token + head * p.c.ld_head;
+        // waited for here: on its way past a row that does not see the key, it would have the
+        // loop over the keys begin with a wait for all loads
+        if constexpr (Q8)
+            scale = in_place(used_scale<DT, Q8>(p.c.vs[page * p.c.lds_page + at.in * p.c.lds_token + head * p.c.lds_head]));
     }
     __device__ __forceinline__ float not_finite(int d) const {
         d = d < dim ? d : dim - 1;  // what lies beyond is not stored
-        float f;
-        if constexpr (Q8)
-            f = (v[d] & 0x7f) == 0x7f ? __builtin_nanf("") : 0.0f;
-        else
-            f = Elem<DT>::to_f32(reinterpret_cast<const typename Elem<DT>::T*>(v)[d]);
+        if constexpr (Q8) {
+            const float f = __builtin_amdgcn_cvt_f32_fp8((uint8_t)v[d], 0) * scale;
+            return fabsf(f) <= (DT == DT_F16 ? 65504.0f : 0x1.fep127f) ? 0.0f : f * INFINITY;
+        }
+        const float f = Elem<DT>::to_f32(reinterpret_cast<const typename Elem<DT>::T*>(v)[d]);
         return __builtin_isfinite(f) ? 0.0f : f;
     }
 };

@@ -128,3 +128,25 @@ def test_great_values_that_weights_fall_far_behind(new, group):
         y = ct.kv_attention(q, s.cache, s.lens, s.table, max_len=longest)
         torch.cuda.synchronize()
         check(longest, s, q, y, see)
+
+
+@pytest.mark.parametrize("dtype,size", [(F16, 4e5), (BF16, 3.39e38)], ids=["f16", "bf16"])
+@pytest.mark.parametrize("new,group", ROWS)
+def test_8_bit_values_past_the_range_of_the_type(new, group, dtype, size):
+    """Codes whose scale takes them past the type count as infinite where they are
+    seen and not where they are not, in stages that are seen whole and in others."""
+    length = 333
+    s = Setup([(length, new)], 2, 64, 16, F32, E4M3, seed=9)
+    places = [10, 200, length - 1 - new // 2, length - 1]
+    for i, at in enumerate(places):
+        s.v[0][at, 1, 7 * i] = size
+        s.v[0][at, 1, 7 * i + 1] = -size
+    s.write()
+    k, v = s.held(0)
+    v[:, 1] = torch.where(v[:, 1].abs() > size / 2, v[:, 1] * INF, v[:, 1])
+    q = torch.randn(new, 2 * group, 64, generator=gen(10), device=DEV).to(dtype)
+    see = seen_causal(length, new, 0, 0)
+    for longest in (None, 1, length):
+        y = ct.kv_attention(q, s.cache, s.lens, s.table, max_len=longest)
+        torch.cuda.synchronize()
+        check(longest, s, q, y, see, k, v)
