@@ -989,6 +989,11 @@ def linear_q8(xq, xs, wq, ws, bias=None, act: str = "none", gate=None, residual=
 
 
 # ---- key-value cache and attention: a transformer block between its projections
+def _same_layout(a, b) -> bool:
+    """One distance in every axis that has one."""
+    return all(n <= 1 or x == y for n, x, y in zip(a.shape, a.stride(), b.stride()))
+
+
 class KVCache:
     """A pool of pages for keys and values, k and v [pages, heads, page, dim].
 
@@ -1003,7 +1008,7 @@ class KVCache:
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         T = _side()
-        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride():
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or not _same_layout(k, v):
             raise ValueError("k and v must be [pages, heads, page, dim] of one shape, type and layout")
         q8 = k.dtype is T.e4m3
         if not q8 and (k.dtype is T.f32 or k.dtype not in T.codes):
@@ -1023,7 +1028,7 @@ class KVCache:
                 if s.get_device() != self.index or s.dtype is not T.f32 or s.shape != k.shape[:3]:
                     raise ValueError(f"{name} must be fp32 {list(k.shape[:3])} on the device of k")
             st = k_scale.stride()
-            if v_scale.stride() != st:
+            if not _same_layout(k_scale, v_scale):
                 raise ValueError("k_scale and v_scale must have one layout")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.device, self.dtype = k.device, k.dtype

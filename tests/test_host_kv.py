@@ -211,3 +211,15 @@ def test_caches_that_the_helper_refuses():
         ct.KVCache(e, e)
     with pytest.raises(ValueError, match="scales"):
         ct.KVCache(m(2, 1, 16, 64), m(2, 1, 16, 64), m(2, 1, 16), m(2, 1, 16))
+
+
+def test_an_axis_of_one_has_no_layout():
+    """k and v of the same layout whose axes of one differ in a stride that nothing
+    uses: refused for where they are only."""
+    for shape in ((3, 1, 16, 64), (1, 4, 16, 64), (3, 4, 1, 64), (1, 1, 1, 64)):
+        n = shape[0] * shape[1] * shape[2] * 64
+        st = [shape[1] * shape[2] * 64, shape[2] * 64, 64, 1]
+        k = torch.empty(n, dtype=torch.bfloat16, device="meta").as_strided(shape, st)
+        v = torch.empty(n, dtype=torch.bfloat16, device="meta").as_strided(shape, [s if m > 1 else 5 * s for s, m in zip(st, shape)])
+        with pytest.raises(ValueError, match="on one device"):
+            ct.KVCache(k, v)
