@@ -1187,14 +1187,18 @@ def kv_attention(q, cache: KVCache, lens, table=None, starts=None, max_len=None,
     b = _batch(cache, tokens, lens, starts, table)
     words, tp = 0, None
     if tree is not None:
-        words = 1 if tree.dim() == 1 else tree.shape[-1]
         if tree.get_device() != index:
             raise ValueError("tree must be a GPU tensor on the device of the cache")
-        if tree.dtype is not T.i64 or tree.dim() > 2 or tree.shape[0] != tokens or not tree.is_contiguous() or words >> 31:
+        if tree.dtype is not T.i64 or tree.dim() not in (1, 2) or tree.shape[0] != tokens or not tree.is_contiguous():
             raise ValueError(f"tree must be contiguous int64 [{tokens}] or [{tokens}, words]")
+        words = 1 if tree.dim() == 1 else tree.shape[1]
+        if words >> 31:
+            raise ValueError(f"{words} words do not fit 32 bits")
         tp = tree.data_ptr()
     if not (0 <= window < 1 << 31 and 0 <= sinks < 1 << 31):
         raise ValueError("window and sinks must be counts of 31 bits")
+    if max_len is not None and max_len < 0:
+        raise ValueError("max_len must not be negative")
     mask = None
     if window or sinks or tp is not None:
         keep = ct_kv_mask(window, sinks, tp, words)
