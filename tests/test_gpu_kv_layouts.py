@@ -189,3 +189,20 @@ def test_two_calls_at_once(cdt):
     for w, g in zip(want, got):
         assert all(torch.equal(w, x) for x in g)
     compare(s, qs[0], want[0])
+
+
+@pytest.mark.parametrize("types", TYPES[:2], ids=IDS[:2])
+@pytest.mark.parametrize("dim", [112, 128, 192, 256])
+@pytest.mark.parametrize("new,group", [(1, 1), (3, 4)])
+def test_few_rows_of_one_sequence_with_a_long_table(new, group, dim, types):
+    """What a guide of 2^19 keys and more in all heads chooses, on short lengths too:
+    the table's further columns name a page of other values."""
+    dtype, cdt = types
+    s = Setup([(3000, new)], 8, dim, 64, dtype, cdt, seed=14)
+    s.write()
+    s.table = torch.cat([s.table, s.table[:, :1].expand(1, 1100)], dim=1).contiguous()
+    q = torch.randn(new, 8 * group, dim, generator=gen(15), device=DEV).to(dtype)
+    for window, sinks in ((0, 0), (1 << 18, 0), (70, 2)):
+        y = ct.kv_attention(q, s.cache, s.lens, s.table, window=window, sinks=sinks)
+        torch.cuda.synchronize()
+        compare(s, q, y, window, sinks)
