@@ -4,7 +4,9 @@
 //
 // over the places j that the token sees.  One pass over the keys with the
 // running maximum m of z and the running sum: what has been summed is scaled
-// by exp(m_old - m_new) where m grows.  All of it in units of log2, with exp2.
+// by exp(m_old - m_new) where m grows (Milakov and Gimelshein, "Online normalizer
+// calculation for softmax", 2018), here only by kLag at least.  All of it in units of
+// log2, with exp2.
 //
 // The heads of a group share their keys, so the rows of a product are (token,
 // head of the group) pairs, token by token, and a tile of rows reads a page
@@ -328,14 +330,18 @@ __device__ __forceinline__ bool sees_any(const AttendParams& p, const Tile& t, c
 
 // The maximum of a row in stages [from, to) that has found none: -infinity where it
 // sees nothing there, else the least number.  All its scores are then -infinity (or
-// NaN, as its sums are), and unless others have a greater maximum, its result is
-// 0 / 0 and not that of a row that sees nothing.
+// NaN, as its sums are), and unless other parts have a greater maximum, its result is
+// 0 / 0 and not that of a row that sees nothing: NaN, also where V is infinite, so
+// without other parts its weights' sum l is NaN.
 template <int KT>
-__device__ __forceinline__ float least_maximum(const AttendParams& p, const Tile& t, const Row& row, const Keys& keys, int from, int to) {
+__device__ __forceinline__ void least_maximum(const AttendParams& p, const Tile& t, const Row& row, const Keys& keys, int from, int to,
+                                              float& m, float& l) {
     bool any = false;
     if (from < keys.sinks) any |= sees_any(p, t, row, from * KT, (to < keys.sinks ? to : keys.sinks) * KT);
     if (to > keys.sinks) any |= sees_any(p, t, row, keys.at(from > keys.sinks ? from : keys.sinks) * KT, (keys.at(to - 1) + 1) * KT);
-    return any ? -0x1.fffffep127f : -INFINITY;
+    any = any && m == -INFINITY;
+    l = any && p.parts <= 1 ? __builtin_nanf("") : l;
+    m = any ? -0x1.fffffep127f : m;
 }
 
 // Does every row among tokens [i0, i1] see all of keys [k0, k0 + KT)?
@@ -509,8 +515,8 @@ __device__ __forceinline__ void part_of(const AttendParams& p, int total, int pa
 // than dim: 16 neighbouring keys, read 16 bytes each, then cover all 64 banks.  Those
 // of V lie 64 bytes (mod 256) apart: a transposing read takes 64 bytes of 8 keys.
 //
-// Measured: a prompt of 8192 tokens, 32 heads on 8, dim 128 bf16 572 us (550 GFLOP,
-// 962 TFLOP/s; a library product of 8192^3 reaches 1227), matrix units 44% busy at
+// Measured: a prompt of 8192 tokens, 32 heads on 8, dim 128 bf16 575 us (550 GFLOP,
+// 956 TFLOP/s; a library product of 8192^3 reaches 1227), matrix units 44% busy at
 // the 1.9 GHz that the chip holds.  What bounds it is the products themselves at
 // that clock: without the exponentials a copy took 539 us, without any weights
 // 521, without reading LDS 541.  Long 16-bit caches of single tokens run at
@@ -798,9 +804,9 @@ __global__ __launch_bounds__(WAVES * 64, (DP > 128 ? 1 : 2)) void attend_tile_ke
         add_not_finite(to - 1);
     }
     l += __shfl_xor(l, 32);
-    if constexpr (!Q8)  // NaN is all that is not finite in 8 bits
+    if constexpr (!Q8)  // within the type's range 8 bits have NaN only, which stays NaN
         mend_nan<DT, KT>(p, t, row, keys, head, from, to, 1, o, l, 4 * half, [](int d, int e) { return d * 32 + 8 * (e / 4) + e % 4; });
-    if (__builtin_expect(__any(m == -INFINITY), 0)) m = m == -INFINITY ? least_maximum<KT>(p, t, row, keys, from, to) : m;
+    if (__builtin_expect(__any(m == -INFINITY), 0)) least_maximum<KT>(p, t, row, keys, from, to, m, l);
     const float inv = inverse<DT, Q8>(l, m);
 #pragma unroll
     for (int d = 0; d < DO; ++d)
@@ -816,8 +822,9 @@ __global__ __launch_bounds__(WAVES * 64, (DP > 128 ? 1 : 2)) void attend_tile_ke
 // piece of LDS; no barrier until the waves' sums are joined.  Two workgroups a CU
 // are enough: registers for three or four (__launch_bounds__) took 64 sequences of
 // up to 8192 tokens in e4m3 from 161 to 176 and 206 us.  Measured: that 157 us
-// (723 MB, 4.6 TB/s), 100 windows of 1024 fp16 28 (106 MB), one token of 1200
-// bf16 12 with the join, a chain of five reads that wait for each other.
+// (723 MB, 4.6 TB/s), 100 windows of 1024 fp16 24.5 (106 MB), 64 sequences of up to 8192
+// bf16 333, one token of 1200 bf16 11.5 with the join, a chain of five reads that wait
+// for each other.
 template <int DT, bool Q8, int DP>
 __global__ __launch_bounds__(256) void attend_rows_kernel(AttendParams p) {
     constexpr int WAVES = 4, KT = 32, ROWS = 16;
@@ -1013,7 +1020,7 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendParams p) {
         total += mw == -INFINITY ? 0.0f : s_ml[w][col][1] * __builtin_amdgcn_exp2f(mw - mx);
     }
     const float fall = fall_to(m, mx);
-    if (__builtin_expect(__any(mx == -INFINITY), 0)) mx = mx == -INFINITY ? least_maximum<KT>(p, t, row, keys, from, to) : mx;
+    if (__builtin_expect(__any(mx == -INFINITY), 0)) least_maximum<KT>(p, t, row, keys, from, to, mx, total);
     if (!Q8 && __builtin_expect(__any(fall == 0.0f), 0)) {
 #pragma unroll
         for (int d = 0; d < DO; ++d)
@@ -1106,7 +1113,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p) {
 #pragma unroll
         for (int w = 1; w < W; ++w) sum += s_o[w][lane];
     }
-    const float inv = inverse<DT, Q8>(total, mx);
+    const float inv = inverse<DT, Q8>(total == 0.0f ? __builtin_nanf("") : total, mx);  // 0 / 0 where V is infinite too
     if (!on) return;
     const uint2v w = {pack2<DT>(sum[0] * inv, sum[1] * inv), pack2<DT>(sum[2] * inv, sum[3] * inv)};
     __builtin_memcpy(p.y + token * p.y_token + head * p.y_head + lane * 8, &w, 8);

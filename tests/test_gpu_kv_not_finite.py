@@ -150,3 +150,32 @@ def test_8_bit_values_past_the_range_of_the_type(new, group, dtype, size):
         y = ct.kv_attention(q, s.cache, s.lens, s.table, max_len=longest)
         torch.cuda.synchronize()
         check(longest, s, q, y, see, k, v)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=str)
+@pytest.mark.parametrize("new,group", ROWS)
+def test_infinities_behind_scores_of_minus_infinity(new, group, dtype):
+    """0 / 0 stays NaN where a value is infinite, in one part and in several; a token
+    with another score has the infinity."""
+    for length in (300, 3000):
+        s = Setup([(length, new)], 1, 64, 64, dtype, dtype, seed=11)
+        s.k[0][:, 0, 5] = -INF
+        s.v[0][:, 0, 3] = INF
+        s.v[0][7, 0, 9] = -INF
+        s.write()
+        q = torch.randn(new, group, 64, generator=gen(12), device=DEV).to(dtype)
+        q[:, :, 5] = 1.0
+        for longest in (None, 1):
+            y = ct.kv_attention(q, s.cache, s.lens, s.table, max_len=longest)
+            torch.cuda.synchronize()
+            assert bool(y.isnan().all()), (length, longest)
+        s.k[0][0, 0, 5] = 1.0
+        s.write()
+        for longest in (None, 1):
+            y = ct.kv_attention(q, s.cache, s.lens, s.table, max_len=longest)
+            torch.cuda.synchronize()
+            # one key has all the weight, but for infinities; a prompt's first tokens do not see place 7
+            want = s.v[0][0, 0].expand(new, group, 64).clone()
+            want[:, :, 3] = INF
+            want[max(0, 7 - (length - new)):, :, 9] = -INF
+            assert torch.equal(y, want), (length, longest)
