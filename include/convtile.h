@@ -498,8 +498,9 @@ typedef struct ct_kv_batch {
  * CT_BF16), into their places: rounded to a 16-bit cache's type, or to e4m3 as
  * above.  *_token and *_head are distances in elements (slices of a fused
  * projection's rows will do).  A token whose place or page does not exist is
- * left out.  Two tokens of a call must not have one place: no page may be two
- * sequences' where they write.  Neither may overlap the cache.
+ * left out.  Two tokens of a call must not have one place, unless their rows are
+ * equal: no page may be two sequences' where they write other rows.  Neither k nor v
+ * may overlap the cache.
  * tokens = 0 is a legal call that does nothing.  None of the calls of this section
  * allocates, synchronises or needs the device to have been set up: all may be
  * captured as a stream's first work.

@@ -1168,7 +1168,9 @@ def kv_attention(q, cache: KVCache, lens, table=None, starts=None, max_len=None,
     nodes: node i sees the context before them and node j if bit j of its row is
     set, its own included.  max_len, the longest of lens where the program
     knows, guides how the work is divided (the table's reach by default); scale is
-    dim ** -0.5 by default.  A token that sees nothing gives zeros."""
+    dim ** -0.5 by default.  A token that sees nothing gives zeros; rows of tokens
+    that belong to no sequence are left as they are (out may name the tensor to
+    write, in a new one they hold what memory held)."""
     T = _side()
     index = cache.index
     if q.dim() != 3:

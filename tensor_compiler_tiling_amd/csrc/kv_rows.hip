@@ -20,9 +20,9 @@
 // Bound by memory.  LPR lanes hold a row, 8 elements each, and a group of them
 // does a token's key and its value, so that two loads are in flight and the
 // place is looked up once.  Measured: 32768 tokens of 8 heads of 128 from bf16 to
-// e4m3 49 us (203 MB, 4.1 TB/s; 52 with a token's heads in a workgroup, whose
-// scales' lines several then write), back 46 us (4.4 TB/s); 2 and 4 tokens a group
-// of lanes 50 and 58 us; a step of 48 tokens 3.9 us.
+// e4m3 48 us (203 MB, 4.2 TB/s; 50 with a token's heads in a workgroup, whose
+// scales' lines several then write), back 45 us (4.5 TB/s); 2 and 4 tokens a group
+// of lanes 50 and 58 us; a step of 48 tokens 3.6 us on the device.
 #include "kv_device.hpp"
 
 namespace ct {
